@@ -20,6 +20,10 @@ JD_ERR_CAPACITY, JD_ERR_CUDA, JD_ERR_DEVICE_STATUS, JD_ERR_IO = 5, 6, 7, 8
 JD_PREC_BF16, JD_PREC_FP32, JD_PREC_FP8 = 0, 1, 2
 JD_SCORER_MLP, JD_SCORER_LINEAR = 0, 1
 JD_ACT_RELU, JD_ACT_GELU = 0, 1
+JD_F32, JD_F16, JD_BF16 = 0, 1, 2
+JD_ROTARY_HALF, JD_ROTARY_INTERLEAVED = 0, 1
+JD_SCALING_NONE, JD_SCALING_LINEAR, JD_SCALING_NTK, JD_SCALING_YARN = 0, 1, 2, 3
+JD_NORM_RMS, JD_NORM_LAYER = 0, 1
 
 i32p = C.POINTER(C.c_int32)
 f32p = C.POINTER(C.c_float)
@@ -69,6 +73,26 @@ class jd_route_request(C.Structure):
 class jd_route_outputs(C.Structure):
     _fields_ = [("winner", i32p), ("winner_p", f32p), ("final_candidates", i32p), ("final_probs", f32p),
                 ("rows_per_round", i32p), ("max_rounds", C.c_int32), ("n_rounds", C.c_int32)]
+
+
+class jd_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("n_heads", C.c_int32)]
+
+
+class jd_rotary_config(C.Structure):
+    _fields_ = [("layout", C.c_int32), ("dims", C.c_int32), ("theta", C.c_double), ("scaling", C.c_int32),
+                ("original_length", C.c_int32), ("factor", C.c_double), ("beta_fast", C.c_double),
+                ("beta_slow", C.c_double)]
+
+
+class jd_rotary_args(C.Structure):
+    _fields_ = [("rotary", jd_rotary_config), ("dtype", C.c_int32), ("head_dim", C.c_int32), ("n_tokens", C.c_int32),
+                ("n_rows", C.c_int32), ("positions", C.c_void_p), ("cu_seqlens", C.c_void_p), ("q", jd_heads),
+                ("k", jd_heads), ("q_out", jd_heads), ("k_out", jd_heads)]
+
+
+class jd_head_norm(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("eps", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p)]
 
 
 # jd_route_scorer: (user, rows, n_rows, probs) -> jd_status
@@ -137,6 +161,10 @@ def lib():
     L.jd_last_launch_count.restype = C.c_int32
     L.jd_set_profiling.argtypes = [C.c_void_p, C.c_int]
     L.jd_profile_report.argtypes = [C.c_void_p, C.c_char_p, C.c_size_t]
+    L.jd_rotary.argtypes = [C.POINTER(jd_rotary_args), C.c_void_p]
+    L.jd_qk_norm_rotary.argtypes = [C.POINTER(jd_rotary_args), C.POINTER(jd_head_norm), C.c_void_p]
+    for name in ("jd_rotary", "jd_qk_norm_rotary"):
+        getattr(L, name).restype = C.c_int
     for name in ("jd_serialize", "jd_model_create", "jd_model_create_shared", "jd_decide", "jd_forward", "jd_decide_host",
                  "jd_decide_packed_host", "jd_check_status", "jd_set_graph_mode", "jd_graph_stats", "jd_set_profiling",
                  "jd_profile_report"):
@@ -372,6 +400,88 @@ def jd_route_scored(requests, score):
         raise err[0]
     _check(code)
     return _route_result(o, s)
+
+
+# ---------------------------------------------------------------- operators
+
+_DTYPES = {"torch.float32": JD_F32, "torch.float16": JD_F16, "torch.bfloat16": JD_BF16}
+_LAYOUTS = {"half": JD_ROTARY_HALF, "interleaved": JD_ROTARY_INTERLEAVED}
+_SCALINGS = {"none": JD_SCALING_NONE, "linear": JD_SCALING_LINEAR, "ntk": JD_SCALING_NTK, "yarn": JD_SCALING_YARN}
+_NORMS = {"rms": JD_NORM_RMS, "layer": JD_NORM_LAYER}
+
+
+def _bad(msg):
+    return JDError(JD_ERR_INVALID_ARG, msg)
+
+
+def _dtype(t):
+    try:
+        return _DTYPES[str(t.dtype)]
+    except KeyError:
+        raise _bad(f"unsupported dtype {t.dtype}") from None
+
+
+def _heads(t, like=None):
+    """jd_heads of a [tokens, heads, head_dim] tensor; `like`: the (shape, dtype) it must have."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
+        raise _bad(f"a [tokens, heads, head_dim] tensor with contiguous heads is required, got {tuple(shape)}")
+    if like is not None and (shape != like[0] or t.dtype != like[1]):
+        raise _bad(f"a tensor is {tuple(shape)} {t.dtype}, not {tuple(like[0])} {like[1]}")
+    return jd_heads(t.data_ptr(), stride[0], stride[1], shape[1])
+
+
+def _vector(t, dtype, n, name):
+    """Pointer of a contiguous vector of n elements (None passes through)."""
+    if t is None:
+        return None
+    if str(t.dtype) != dtype or t.numel() != n or not t.is_contiguous():
+        raise _bad(f"{name}: a contiguous {dtype} tensor of {n} elements is required")
+    return t.data_ptr()
+
+
+def rotary_config(dims, theta, layout="half", scaling="none", factor=1.0, original_length=8192, beta_fast=32.0,
+                  beta_slow=1.0):
+    """jd_rotary_config; layout and scaling by name ("half" / "interleaved", "none" / "linear" / "ntk" / "yarn")."""
+    try:
+        return jd_rotary_config(_LAYOUTS[layout], dims, theta, _SCALINGS[scaling], original_length, factor, beta_fast,
+                                beta_slow)
+    except KeyError as e:
+        raise _bad(f"unknown rotary layout or scaling {e}") from None
+
+
+def _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions):
+    hq = _heads(q)
+    T, _, d = q.shape
+    if k is None:
+        hk = hko = jd_heads()
+    else:
+        hk = _heads(k)
+        if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or k_out is None:
+            raise _bad("k must have q's tokens, head_dim and dtype, and an output")
+        hko = _heads(k_out, (k.shape, k.dtype))
+    n_rows = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    return jd_rotary_args(rotary, _dtype(q), d, T, n_rows, _vector(positions, "torch.int32", T, "positions"),
+                          _vector(cu_seqlens, "torch.int32", n_rows + 1, "cu_seqlens"), hq, hk,
+                          _heads(q_out, (q.shape, q.dtype)), hko)
+
+
+def jd_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=None, positions=None, stream=None):
+    """Rotate q and k (device tensors [tokens, heads, head_dim]; k may be None) into q_out and k_out, which may be
+    q and k themselves.  Positions: `positions` (int32 per token), else the index in the row from `cu_seqlens`."""
+    a = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
+    _check(lib().jd_rotary(C.byref(a), _stream(stream)))
+
+
+def jd_qk_norm_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=None, positions=None, norm="rms",
+                      eps=1e-5, q_gain=None, k_gain=None, stream=None):
+    """jd_rotary with a norm ("rms" or "layer", gains float32 [head_dim] or None) of every head before the rotation."""
+    a = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
+    if norm not in _NORMS:
+        raise _bad(f"unknown norm {norm!r}")
+    n = jd_head_norm(_NORMS[norm], eps, _vector(q_gain, "torch.float32", a.head_dim, "q_gain"),
+                     _vector(k_gain, "torch.float32", a.head_dim, "k_gain"))
+    _check(lib().jd_qk_norm_rotary(C.byref(a), C.byref(n), _stream(stream)))
 
 
 class Model:

@@ -424,6 +424,97 @@ jd_status jd_forward_noalloc(jd_model *model, const jd_batch *batch, float *logi
  * model, FP32 model), JD_ERR_CUDA (the synchronization or copy failed). */
 jd_status jd_noalloc_check_status(jd_model *model, void *stream);
 
+/* ---------------------------------------------------------------- operators
+ *
+ * The operators of an encoder layer between its QKV projection and its output
+ * projection, on the caller's device buffers: rotary positions, norms of the
+ * query and key heads with the rotation in the same pass, and differential
+ * attention.  A model whose weights file carries their tensors runs them in
+ * place of its plain rotation and attention (see jd_model_create); these calls
+ * run them on their own.
+ *   - They keep no state: no workspace, no allocation, nothing read back.  Work
+ *     is queued on `stream` and may be captured into a CUDA graph.  Calls may
+ *     overlap on different streams as far as their buffers allow.
+ *   - They run on the device that holds the buffers, whichever is current, and
+ *     leave the caller's current device as it was; `stream` must belong to the
+ *     buffers' device (NULL: its legacy default stream).
+ *   - Forward only: the library computes no gradients.
+ *   - Errors: JD_ERR_INVALID_ARG (what each call states; a pointer that is not
+ *     device memory, buffers of two devices), JD_ERR_CUDA (no device, not
+ *     sm_100, a launch failed).  Nothing is written on an argument error. */
+typedef enum { JD_F32 = 0, JD_F16 = 1, JD_BF16 = 2 } jd_dtype;
+
+/* The heads of one tensor over packed tokens, in device memory: element i of
+ * head h of token t is data[t * token_stride + h * head_stride + i].  Strides
+ * count elements, not bytes; a q|k|v row of 1152 has token_stride 1152 and
+ * head_stride 64.  The elements of a head are contiguous.  An output's strides
+ * must keep its elements apart; an input may repeat (stride 0). */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+    int32_t n_heads;
+} jd_heads;
+
+enum { JD_ROTARY_HALF = 0, JD_ROTARY_INTERLEAVED = 1 };
+enum { JD_SCALING_NONE = 0, JD_SCALING_LINEAR = 1, JD_SCALING_NTK = 2, JD_SCALING_YARN = 3 };
+
+/* Rotary positions.  With r = dims, pair j < r/2 of a head at position p turns
+ * by p * w_j, w_j = theta^(-2j/r):
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * JD_ROTARY_HALF pairs elements (j, j + r/2), JD_ROTARY_INTERLEAVED (2j, 2j+1);
+ * elements r .. head_dim - 1 pass through.  Scaling stretches the positions of
+ * a trained length over rows `factor` times as long:
+ *   LINEAR  w_j / factor
+ *   NTK     theta * factor^(r / (r - 2)) in place of theta
+ *   YARN    w_j (1 - g_j) + w_j / factor * g_j with g_j rising linearly from 0
+ *           to 1 between the pairs that turn beta_fast and beta_slow times over
+ *           original_length (rounded outwards, kept within [0, r - 1]), and
+ *           both cos and sin times 0.1 ln(factor) + 1 when factor > 1.
+ * Angles are formed and reduced in 64 bits, so far positions keep their
+ * accuracy. */
+typedef struct {
+    int32_t layout;           /* JD_ROTARY_HALF or JD_ROTARY_INTERLEAVED */
+    int32_t dims;             /* r: even, 2 .. head_dim */
+    double theta;             /* > 0 (YARN: > 1) */
+    int32_t scaling;          /* JD_SCALING_* */
+    int32_t original_length;  /* YARN: the trained length, >= 1 */
+    double factor;            /* > 0; ignored without scaling */
+    double beta_fast, beta_slow; /* YARN: 32 and 1 usually; beta_fast > beta_slow > 0 */
+} jd_rotary_config;
+
+/* Queries and keys of n_tokens packed tokens.  Positions are positions[t]
+ * where given (device, [n_tokens]; cu_seqlens is then not read), else the
+ * token's index in its row, from cu_seqlens (device, [n_rows + 1], ascending
+ * from 0): tokens past cu_seqlens[n_rows] are left alone, read or written.
+ * q_out / k_out may be q / k themselves (the same pointer and strides: in
+ * place) or must not overlap any input or each other.  k.n_heads = 0: queries
+ * only. */
+typedef struct {
+    jd_rotary_config rotary;
+    int32_t dtype;            /* jd_dtype of q, k and their outputs */
+    int32_t head_dim;         /* 2 .. 256 */
+    int32_t n_tokens, n_rows; /* >= 0; no tokens: nothing is done */
+    const int32_t *positions, *cu_seqlens;
+    jd_heads q, k, q_out, k_out;
+} jd_rotary_args;
+
+/* Rotate the queries and keys.  Arithmetic is FP32, rounded once to dtype. */
+jd_status jd_rotary(const jd_rotary_args *args, void *stream);
+
+enum { JD_NORM_RMS = 0, JD_NORM_LAYER = 1 };
+
+/* Norm of every head over its head_dim elements: x / sqrt(mean x^2 + eps) *
+ * gain (JD_NORM_RMS) or (x - mean) / sqrt(variance + eps) * gain
+ * (JD_NORM_LAYER, biased variance). */
+typedef struct {
+    int32_t kind;
+    float eps;                /* >= 0 */
+    const float *q_gain, *k_gain; /* device [head_dim], or NULL for 1 */
+} jd_head_norm;
+
+/* Normalise every query and key head, then rotate it, in one pass over memory. */
+jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
