@@ -1,15 +1,21 @@
 // Rotary positions, with or without a norm of every head in the same pass.
 //
-// A warp takes one token: all its query and key heads turn by the same angles, so the warp forms
-// the r/2 sines and cosines once (a lane per pair) and passes them on through shared memory.  The
-// token's heads then go by in groups: head_dim / 8 lanes (up to the next power of two) hold one
-// head, eight elements a lane, so that a head's norm is a few shuffles and a lane's loads and
-// stores are 16 bytes.  Up to four groups are loaded before the first is worked on.
+// All heads of a token turn by the same angles.  A token's threads (all in one warp) form its r/2
+// sines and cosines once and share them through shared memory; each thread then turns the same
+// eight pairs of one head after another, with the sines in registers.  Its sixteen elements are two
+// 16-byte loads (four in FP32) and never leave the thread: consecutive elements hold eight
+// interleaved pairs, two runs of eight elements half = r/2 apart hold eight pairs of the half layout.
+// A head's norm is a sum over the thread's elements and a few shuffles.  A thread's next heads are
+// always on their way into shared memory (cp.async), also across tokens: with them in registers
+// the kernel took 114 of those, 16 warps an SM.
 //
-// The pass is bound by HBM: it reads and writes each element once.  Computing the angles instead
-// of reading a table costs a fifth of the issue slots that the memory time leaves free and keeps
-// any position exact: p * w_j is formed and reduced to a fraction of a turn in 64 bits (in 32 bits
-// the angle of position 10^5 is off by 4e-3), sine and cosine of the fraction are then FP32.
+// The pass reads and writes each element once and is bound by HBM.  Forming the angles beats
+// reading a table: p * w_j is reduced to a fraction of a turn in 64 bits, exact for any position (in
+// 32 bits the angle at position 10^5 is off by 4e-3), and sine and cosine of the fraction are FP32.
+//
+// Two kernels: k_rotary as above, where head_dim and the two runs fall on 16-byte vectors, and
+// k_rotary_any for every other width, offset and stride (a head through shared memory, eight
+// elements a lane).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,8 +31,6 @@ namespace jd {
 namespace {
 
 constexpr int WARPS = 8;
-
-enum Pairing { INTERLEAVED, HALF_LANES, HALF_SHARED };
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -45,29 +49,98 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
+// Eight elements as they lie in memory, in registers.
 template <typename T>
-struct alignas(16) Vec8 {
-    T v[8];
+struct Vec8 {
+    static constexpr int N = sizeof(T) / 2;
+    uint4 v[N];
 };
+
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t u, float &lo, float &hi);
+template <>
+__device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t u, float &lo, float &hi) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void unpack2<__half>(uint32_t u, float &lo, float &hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    lo = f.x;
+    hi = f.y;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Vec8<T> &x, float *y) {
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::N; ++i) {
+        const uint32_t u[4] = {x.v[i].x, x.v[i].y, x.v[i].z, x.v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4) y[4 * i + j] = __uint_as_float(u[j]);
+            else unpack2<T>(u[j], y[2 * j], y[2 * j + 1]);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> pack8(const float *y) {
+    Vec8<T> x;
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::N; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4) u[j] = __float_as_uint(y[4 * i + j]);
+            else u[j] = pack2<T>(y[2 * j], y[2 * j + 1]);
+        }
+        x.v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    return x;
+}
+// Elements that are read once need not stay in the caches.
+template <typename T>
+__device__ __forceinline__ Vec8<T> stream8(const T *p) {
+    Vec8<T> x;
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::N; ++i) x.v[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    return x;
+}
+template <typename T>
+__device__ __forceinline__ void put8(T *p, const Vec8<T> &x) {
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::N; ++i) reinterpret_cast<uint4 *>(p)[i] = x.v[i];
+}
 
 // Eight elements of a head from element e0 on; past head_dim zeros are read and nothing is written.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(Vec8<T> &x, const T *p, int e0, int head_dim) {
+__device__ __forceinline__ void load8(float *y, const T *p, int e0, int head_dim) {
     if (VEC) {
-        x = *reinterpret_cast<const Vec8<T> *>(p + e0);
+        unpack8(stream8(p + e0), y);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x.v[j] = e0 + j < head_dim ? p[e0 + j] : from_f<T>(0.f);
+        for (int j = 0; j < 8; ++j) y[j] = e0 + j < head_dim ? to_f(p[e0 + j]) : 0.f;
     }
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *p, const Vec8<T> &x, int e0, int head_dim) {
+__device__ __forceinline__ void store8(T *p, const float *y, int e0, int head_dim) {
     if (VEC) {
-        *reinterpret_cast<Vec8<T> *>(p + e0) = x;
+        put8(p + e0, pack8<T>(y));
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (e0 + j < head_dim) p[e0 + j] = x.v[j];
+            if (e0 + j < head_dim) p[e0 + j] = from_f<T>(y[j]);
     }
 }
 
@@ -88,13 +161,278 @@ __device__ __forceinline__ int row_of(const int *cu, int n_rows, int t, int lane
     return cu[lo] <= t ? lo : -1;
 }
 
-template <typename T, Pairing PAIR, bool NORM, bool VEC>
-__global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ RotaryOp op) {
+__device__ __forceinline__ void load8f(const float *p, float *y) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+}
+
+// Two FP32 operations an instruction (sm_100 f32x2 forms).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ void copy_async16(void *shared, const void *global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+                 "l"(global)
+                 : "memory");
+}
+
+// Sixteen elements of a thread (two runs of eight) as eight pairs, and back.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void split_pairs(const float *y, float2 *a, float2 *b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        a[j] = INTERLEAVED ? make_float2(y[4 * j], y[4 * j + 2]) : make_float2(y[2 * j], y[2 * j + 1]);
+        b[j] = INTERLEAVED ? make_float2(y[4 * j + 1], y[4 * j + 3]) : make_float2(y[8 + 2 * j], y[9 + 2 * j]);
+    }
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void join_pairs(float *z, const float2 *a, const float2 *b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        z[INTERLEAVED ? 4 * j : 2 * j] = a[j].x;
+        z[INTERLEAVED ? 4 * j + 2 : 2 * j + 1] = a[j].y;
+        z[INTERLEAVED ? 4 * j + 1 : 8 + 2 * j] = b[j].x;
+        z[INTERLEAVED ? 4 * j + 3 : 9 + 2 * j] = b[j].y;
+    }
+}
+
+constexpr int VWARPS = 4;         // warps of a k_rotary CTA
+constexpr int AHEAD = 3;          // heads on their way to each thread
+constexpr int CTAS_PER_SM = 32;   // CTAs of a launch, at most, for each SM
+
+// NORM: 0 none, 1 RMS, 2 layer norm
+template <typename T, bool INTERLEAVED, int NORM>
+__global__ void __launch_bounds__(32 * VWARPS) k_rotary(const __grid_constant__ RotaryOp op) {
+    // heads on their way, in 16-byte pieces: each thread reads only what it asked for.  One place
+    // more than are on their way, so that none is overwritten in the turn that reads it.
+    constexpr int PIECES = 2 * Vec8<T>::N;
+    __shared__ uint4 ring[AHEAD + 1][PIECES][32 * VWARPS];
+    // cosines, sines of the CTA's tokens: 32 * VWARPS threads of at most eight pairs each
+    __shared__ __align__(16) float cosines[32 * VWARPS * 8], sines[32 * VWARPS * 8];
+    __shared__ double turns[ROTARY_MAX_PAIRS];
+    const int lane = threadIdx.x & 31;
+    const int L = op.lanes_per_head, HS = op.heads_at_once, TPT = L * HS;  // powers of two, TPT <= 32
+    const int in_token = threadIdx.x & (TPT - 1), unit = in_token & (L - 1), hs = in_token / L;
+    const int r = op.dims, half = r >> 1, turning = r >> 4;  // half layout: threads of a head that turn
+    const int n_heads = op.n_heads[0] + op.n_heads[1];
+    // This thread's two runs of eight elements: half of what they divide apart, so that neighbouring
+    // threads touch neighbouring 16 bytes (32-byte steps cost a third of the bandwidth).
+    const int low = INTERLEAVED || unit < turning ? 0 : r, wide = INTERLEAVED ? op.head_dim : (low ? op.head_dim - r : r);
+    const int e0 = low + 8 * (unit - (low >> 4)), e1 = e0 + (wide >> 1);
+    const bool live = 16 * unit < op.head_dim;
+    // its eight pairs' sines: the half layout's from 8 * unit on, the interleaved ones' with their runs
+    const int pair0 = INTERLEAVED ? e0 >> 1 : 8 * unit, pair4 = INTERLEAVED ? e1 >> 1 : 8 * unit + 4;
+    const int turns0 = live ? min(4, max(0, half - pair0)) : 0, turns4 = live ? min(4, max(0, half - pair4)) : 0;
+    const bool on = live && !(NORM == 0 && op.in_place && turns0 + turns4 == 0);
+    const float inv_n = 1.0f / (float)op.head_dim;
+    const int slot = (threadIdx.x / TPT) * (8 * L);  // this token's sines
+    for (int j = threadIdx.x; j < half; j += 32 * VWARPS) turns[j] = op.turns[j];
+    __syncthreads();
+    // a CTA walks consecutive tokens, each warp 32 / TPT at a time, and follows their rows
+    const int at_once = 32 / TPT, step = VWARPS * at_once;
+    const int begin = blockIdx.x * op.tokens_per_cta, last = min(op.n_tokens, begin + op.tokens_per_cta);
+    const int first = begin + (threadIdx.x >> 5) * at_once;
+    if (first >= last) return;
+
+    // where head hs of a token lies among the queries, and where it would lie among the keys
+    auto queries = [&](const void *base, int64_t token, int64_t head, int t) {
+        return static_cast<const T *>(base) + t * token + hs * head + e0;
+    };
+    auto keys = [&](const void *base, int64_t token, int64_t head, int t) {
+        return static_cast<const T *>(base) + t * token + (hs - op.n_heads[0]) * head + e0;
+    };
+    // the next head to ask for: an index, its token, and the two places
+    int next_t = first + lane / TPT, next_h = hs, next_place = 0;
+    const T *next_q = queries(op.src[0], op.src_token[0], op.src_head[0], next_t);
+    const T *next_k = keys(op.src[1], op.src_token[1], op.src_head[1], next_t);
+    auto ask = [&]() {
+        if (on && next_t < last && next_h < n_heads) {
+            const T *p = next_h < op.n_heads[0] ? next_q : next_k;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+                copy_async16(&ring[next_place][i][threadIdx.x],
+                             reinterpret_cast<const uint4 *>(i < PIECES / 2 ? p : p + (e1 - e0)) + i % (PIECES / 2));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next_place = next_place == AHEAD ? 0 : next_place + 1;
+        next_h += HS;
+        next_q += HS * op.src_head[0];
+        next_k += HS * op.src_head[1];
+        if (next_h - hs >= n_heads) {
+            next_h = hs;
+            next_t += step;
+            next_q = queries(op.src[0], op.src_token[0], op.src_head[0], next_t);
+            next_k = keys(op.src[1], op.src_token[1], op.src_head[1], next_t);
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < AHEAD; ++i) ask();
+
+    int row = -1, row_start = 0, row_end = op.n_tokens;
+    if (!op.positions) {
+        row = row_of(op.cu, op.n_rows, first, lane);
+        row_start = row < 0 ? 0 : op.cu[row];
+        row_end = row < 0 ? 0 : op.cu[row + 1];  // past every row: nothing to do, and nothing follows
+    }
+    int place = 0;
+    for (int t0 = first; t0 < last; t0 += step) {
+        const int t = t0 + lane / TPT;
+        bool work = on && t < last;
+        int pos = 0;
+        if (op.positions) {
+            if (t < last) pos = op.positions[t];
+        } else {
+            while (row >= 0 && t >= row_end && row + 1 < op.n_rows) {
+                ++row;
+                row_start = row_end;
+                row_end = op.cu[row + 1];
+            }
+            work = work && t < row_end;
+            pos = t - row_start;
+        }
+        __syncwarp();  // the last tokens' sines have been read
+        for (int j = in_token; j < half; j += TPT) {
+            double a = (double)pos * turns[j];
+            a -= rint(a);
+            float s, c;
+            sincospif(2.0f * (float)a, &s, &c);
+            cosines[slot + j] = op.amplitude * c;
+            sines[slot + j] = op.amplitude * s;
+        }
+        __syncwarp();
+        float2 c[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const int at = slot + (j ? pair4 : pair0);
+            const float4 c4 = *reinterpret_cast<const float4 *>(&cosines[at]), s4 = *reinterpret_cast<const float4 *>(&sines[at]);
+            c[j] = make_float2(c4.x, c4.y), c[j + 1] = make_float2(c4.z, c4.w);
+            s[j] = make_float2(s4.x, s4.y), s[j + 1] = make_float2(s4.z, s4.w);
+        }
+
+        T *out_q = const_cast<T *>(queries(op.dst[0], op.dst_token[0], op.dst_head[0], t));
+        T *out_k = const_cast<T *>(keys(op.dst[1], op.dst_token[1], op.dst_head[1], t));
+#pragma unroll 1
+        for (int h = hs; h - hs < n_heads; h += HS, out_q += HS * op.dst_head[0], out_k += HS * op.dst_head[1]) {
+            ask();
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+            // eight pairs (a_j, b_j), two and two: the first elements in ya, the second in yb
+            float2 ya[4], yb[4];
+            {
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    Vec8<T> x;
+#pragma unroll
+                    for (int j = 0; j < PIECES / 2; ++j) x.v[j] = ring[place][i * (PIECES / 2) + j][threadIdx.x];
+                    unpack8(x, y + 8 * i);
+                }
+                split_pairs<INTERLEAVED>(y, ya, yb);
+            }
+            place = place == AHEAD ? 0 : place + 1;
+            const bool mine = work && h < n_heads;
+            const int w = h < op.n_heads[0] ? 0 : 1;
+            if (NORM) {
+                if (!mine) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ya[j] = yb[j] = make_float2(0.f, 0.f);
+                }
+                if (NORM == 2) {
+                    float2 m2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m2 = add2(m2, add2(ya[j], yb[j]));
+                    float m = m2.x + m2.y;
+                    for (int o = L >> 1; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+                    m = live ? -m * inv_n : 0.f;
+                    m2 = make_float2(m, m);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ya[j] = add2(ya[j], m2);
+                        yb[j] = add2(yb[j], m2);
+                    }
+                }
+                float2 q2 = make_float2(0.f, 0.f), p2 = q2;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    q2 = fma2(ya[j], ya[j], q2);
+                    p2 = fma2(yb[j], yb[j], p2);
+                }
+                float q = (q2.x + q2.y) + (p2.x + p2.y);
+                for (int o = L >> 1; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+                const float f = rsqrtf(fmaf(q, inv_n, op.eps));
+                const float2 f2 = make_float2(f, f);
+                const float *g = op.gain[w];
+                if (g && live) {
+                    float ga[16];
+                    load8f(g + e0, ga);
+                    load8f(g + e1, ga + 8);
+                    float2 g0[4], g1[4];
+                    split_pairs<INTERLEAVED>(ga, g0, g1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ya[j] = mul2(ya[j], mul2(f2, g0[j]));
+                        yb[j] = mul2(yb[j], mul2(f2, g1[j]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        ya[j] = mul2(ya[j], f2);
+                        yb[j] = mul2(yb[j], f2);
+                    }
+                }
+            }
+            if (!mine) continue;
+            float2 za[4], zb[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 minus = make_float2(-yb[j].x, -yb[j].y);
+                za[j] = fma2(ya[j], c[j], mul2(minus, s[j]));
+                zb[j] = fma2(yb[j], c[j], mul2(ya[j], s[j]));
+            }
+            if (turns0 + turns4 < 8) {  // what does not turn passes through (0 * inf must not enter)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int some = j < 2 ? turns0 : turns4, first_of = (j & 1) * 2;
+                    if (first_of >= some) za[j].x = ya[j].x, zb[j].x = yb[j].x;
+                    if (first_of + 1 >= some) za[j].y = ya[j].y, zb[j].y = yb[j].y;
+                }
+            }
+            float z[16];
+            join_pairs<INTERLEAVED>(z, za, zb);
+            T *p = w ? out_k : out_q;
+            put8(p, pack8<T>(z));
+            put8(p + (e1 - e0), pack8<T>(z + 8));
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename T, bool INTERLEAVED, bool NORM, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS) k_rotary_any(const __grid_constant__ RotaryOp op) {
     __shared__ float2 cs_all[WARPS][ROTARY_MAX_PAIRS];
-    __shared__ float swap_all[PAIR == HALF_SHARED ? WARPS : 1][PAIR == HALF_SHARED ? 32 * 8 : 1];
+    __shared__ float swap_all[INTERLEAVED ? 1 : WARPS][INTERLEAVED ? 1 : 32 * 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float2 *cs = cs_all[warp];
-    float *swap = swap_all[PAIR == HALF_SHARED ? warp : 0];
+    float *swap = swap_all[INTERLEAVED ? 0 : warp];
     const int r = op.dims, half = r >> 1;
 
     double turns[ROTARY_MAX_PAIRS / 32];
@@ -111,16 +449,43 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
     // in place and without a norm the elements past r keep their values where they are
     const bool skip = !live || (!NORM && op.in_place && e0 >= r);
     const float inv_n = 1.0f / (float)op.head_dim;
-    const int partner = PAIR == HALF_LANES ? (e0 < half ? lane + (half >> 3) : lane - (half >> 3)) : lane;
 
-    for (int t = blockIdx.x * WARPS + warp; t < op.n_tokens; t += gridDim.x * WARPS) {
+    // a CTA walks consecutive tokens, a warp one at a time, and follows their rows
+    const int begin = blockIdx.x * op.tokens_per_cta, last = min(op.n_tokens, begin + op.tokens_per_cta);
+    if (begin + warp >= last) return;
+    int row = -1, row_start = 0, row_end = op.n_tokens;
+    if (!op.positions) {
+        row = row_of(op.cu, op.n_rows, begin + warp, lane);
+        if (row < 0) return;
+        row_start = op.cu[row];
+        row_end = op.cu[row + 1];
+    }
+    for (int t = begin + warp; t < last; t += WARPS) {
+        float x[4][8];
+        auto load = [&](int h0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int hh = h0 + u * heads_at_once + sub;
+                if (hh < n_heads && !skip) {
+                    const int w = hh < op.n_heads[0] ? 0 : 1;
+                    const int h = w ? hh - op.n_heads[0] : hh;
+                    load8<T, VEC>(x[u], static_cast<const T *>(op.src[w]) + t * op.src_token[w] + h * op.src_head[w], e0,
+                                  op.head_dim);
+                }
+            }
+        };
+        load(0);
         int pos;
         if (op.positions) {
             pos = op.positions[t];
         } else {
-            const int row = row_of(op.cu, op.n_rows, t, lane);
-            if (row < 0) continue;
-            pos = t - op.cu[row];
+            while (t >= row_end && row + 1 < op.n_rows) {
+                ++row;
+                row_start = row_end;
+                row_end = op.cu[row + 1];
+            }
+            if (t >= row_end) return;
+            pos = t - row_start;
         }
 #pragma unroll
         for (int i = 0; i < ROTARY_MAX_PAIRS / 32; ++i) {
@@ -137,8 +502,8 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = e0 + j;
-            const bool first = PAIR == INTERLEAVED ? (e & 1) == 0 : e < half;
-            const int pair = PAIR == INTERLEAVED ? e >> 1 : (first ? e : e - half);
+            const bool first = INTERLEAVED ? (e & 1) == 0 : e < half;
+            const int pair = INTERLEAVED ? e >> 1 : (first ? e : e - half);
             const float2 v = e < r ? cs[pair] : make_float2(1.f, 0.f);
             c[j] = v.x;
             s[j] = first ? -v.y : v.y;
@@ -146,17 +511,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
         __syncwarp();
 
         for (int h0 = 0; h0 < n_heads; h0 += 4 * heads_at_once) {
-            Vec8<T> x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int hh = h0 + u * heads_at_once + sub;
-                if (hh < n_heads && !skip) {
-                    const int w = hh < op.n_heads[0] ? 0 : 1;
-                    const int h = w ? hh - op.n_heads[0] : hh;
-                    load8<T, VEC>(x[u], static_cast<const T *>(op.src[w]) + t * op.src_token[w] + h * op.src_head[w], e0,
-                                  op.head_dim);
-                }
-            }
+            if (h0) load(h0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (h0 + u * heads_at_once >= n_heads) break;  // the same for the whole warp
@@ -165,7 +520,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
                 const int w = hh < op.n_heads[0] ? 0 : 1;
                 float y[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = on ? to_f(x[u].v[j]) : 0.f;
+                for (int j = 0; j < 8; ++j) y[j] = on ? x[u][j] : 0.f;
                 if (NORM) {
                     if (op.layer_norm) {
                         float m = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
@@ -182,7 +537,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
 #pragma unroll
                     for (int j = 0; j < 8; ++j) q = fmaf(y[j], y[j], q);
                     for (int o = G >> 1; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-                    const float f = 1.0f / sqrtf(fmaf(q, inv_n, op.eps));
+                    const float f = rsqrtf(fmaf(q, inv_n, op.eps));
                     const float *g = w ? op.gain[1] : op.gain[0];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -191,12 +546,9 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
                     }
                 }
                 float p[8];
-                if (PAIR == INTERLEAVED) {
+                if (INTERLEAVED) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) p[j] = y[j ^ 1];
-                } else if (PAIR == HALF_LANES) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = __shfl_sync(0xffffffffu, y[j], partner);
                 } else {
                     float *mine = swap + sub * G * 8;
 #pragma unroll
@@ -209,10 +561,10 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
                     }
                     __syncwarp();
                 }
-                Vec8<T> z;
+                float z[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)  // past r the partner is another element: it must not enter (0 * inf)
-                    z.v[j] = from_f<T>(e0 + j < r ? fmaf(p[j], s[j], y[j] * c[j]) : y[j]);
+                    z[j] = e0 + j < r ? fmaf(y[j], c[j], p[j] * s[j]) : y[j];
                 if (on) {
                     const int h = w ? hh - op.n_heads[0] : hh;
                     store8<T, VEC>(static_cast<T *>(op.dst[w]) + t * op.dst_token[w] + h * op.dst_head[w], z, e0,
@@ -223,35 +575,57 @@ __global__ void __launch_bounds__(32 * WARPS) k_rotary(const __grid_constant__ R
     }
 }
 
-template <typename T, bool NORM>
-void launch_pairing(const RotaryOp &op, int grid, cudaStream_t st) {
-    const dim3 g(grid), b(32 * WARPS);
+template <typename T, bool INTERLEAVED>
+void launch_typed(const RotaryOp &op, cudaStream_t st) {
     if (op.vec) {
-        if (op.interleaved) k_rotary<T, INTERLEAVED, NORM, true><<<g, b, 0, st>>>(op);
-        else if (op.dims % 16 == 0) k_rotary<T, HALF_LANES, NORM, true><<<g, b, 0, st>>>(op);
-        else k_rotary<T, HALF_SHARED, NORM, true><<<g, b, 0, st>>>(op);
+        const dim3 g(op.ctas), b(32 * VWARPS);
+        if (!op.norm) k_rotary<T, INTERLEAVED, 0><<<g, b, 0, st>>>(op);
+        else if (!op.layer_norm) k_rotary<T, INTERLEAVED, 1><<<g, b, 0, st>>>(op);
+        else k_rotary<T, INTERLEAVED, 2><<<g, b, 0, st>>>(op);
+        return;
+    }
+    const dim3 b(32 * WARPS);
+    const dim3 g(op.ctas);
+    if (op.vec8) {
+        if (op.norm) k_rotary_any<T, INTERLEAVED, true, true><<<g, b, 0, st>>>(op);
+        else k_rotary_any<T, INTERLEAVED, false, true><<<g, b, 0, st>>>(op);
     } else {
-        if (op.interleaved) k_rotary<T, INTERLEAVED, NORM, false><<<g, b, 0, st>>>(op);
-        else k_rotary<T, HALF_SHARED, NORM, false><<<g, b, 0, st>>>(op);
+        if (op.norm) k_rotary_any<T, INTERLEAVED, true, false><<<g, b, 0, st>>>(op);
+        else k_rotary_any<T, INTERLEAVED, false, false><<<g, b, 0, st>>>(op);
     }
 }
 
 template <typename T>
-void launch_norm(const RotaryOp &op, int grid, cudaStream_t st) {
-    if (op.norm) launch_pairing<T, true>(op, grid, st);
-    else launch_pairing<T, false>(op, grid, st);
+void launch_layout(const RotaryOp &op, cudaStream_t st) {
+    if (op.interleaved) launch_typed<T, true>(op, st);
+    else launch_typed<T, false>(op, st);
 }
 
 }  // namespace
 
+void rotary_plan(RotaryOp &op, bool aligned) {
+    // vectors of eight elements throughout; in the half layout also the second run of eight
+    op.vec8 = aligned && op.head_dim % 8 == 0;
+    op.vec = aligned && op.head_dim % 16 == 0 && (op.interleaved || op.dims % 16 == 0);
+    op.lanes_per_head = 1;
+    while (op.lanes_per_head * (op.vec ? 16 : 8) < op.head_dim) op.lanes_per_head *= 2;
+    // heads that a token's threads take at once: four, or as many as there are
+    op.heads_at_once = 1;
+    while (op.heads_at_once < 4 && op.heads_at_once * 2 <= op.n_heads[0] + op.n_heads[1] &&
+           op.heads_at_once * 2 * op.lanes_per_head <= 32)
+        op.heads_at_once *= 2;
+    // tokens of one step of a CTA; at most 32 CTAs an SM, which even out their ends, walk the rest
+    const int per_step = op.vec ? VWARPS * 32 / (op.lanes_per_head * op.heads_at_once) : WARPS;
+    const int steps = (op.n_tokens + per_step - 1) / per_step;
+    op.tokens_per_cta = (steps + 148 * CTAS_PER_SM - 1) / (148 * CTAS_PER_SM) * per_step;
+    op.ctas = (op.n_tokens + op.tokens_per_cta - 1) / op.tokens_per_cta;
+}
+
 cudaError_t launch_rotary(const RotaryOp &op, cudaStream_t st) {
     if (op.n_tokens <= 0) return cudaSuccess;
-    // enough CTAs to fill every SM several times over; beyond that warps walk the tokens
-    const int want = (op.n_tokens + WARPS - 1) / WARPS;
-    const int grid = want < 148 * 8 ? want : 148 * 8;
-    if (op.dtype == JD_F32) launch_norm<float>(op, grid, st);
-    else if (op.dtype == JD_F16) launch_norm<__half>(op, grid, st);
-    else launch_norm<__nv_bfloat16>(op, grid, st);
+    if (op.dtype == JD_F32) launch_layout<float>(op, st);
+    else if (op.dtype == JD_F16) launch_layout<__half>(op, st);
+    else launch_layout<__nv_bfloat16>(op, st);
     return cudaGetLastError();
 }
 
@@ -379,7 +753,7 @@ jd_status rotary_call(const jd_rotary_args *a, const jd_head_norm *norm, void *s
         return fail(JD_ERR_INVALID_ARG, "positions or cu_seqlens is required");
     const jd_heads *in[2] = {&a->q, &a->k}, *out[2] = {&a->q_out, &a->k_out};
     const size_t elem = dtype_bytes(a->dtype);
-    op.vec = a->head_dim % 8 == 0;
+    bool aligned = (((uintptr_t)(norm ? norm->q_gain : nullptr) | (uintptr_t)(norm ? norm->k_gain : nullptr)) & 15) == 0;
     op.in_place = true;
     for (int w = 0; w < 2; ++w) {
         op.n_heads[w] = in[w]->n_heads;
@@ -395,7 +769,7 @@ jd_status rotary_call(const jd_rotary_args *a, const jd_head_norm *norm, void *s
         op.src_head[w] = in[w]->head_stride;
         op.dst_token[w] = out[w]->token_stride;
         op.dst_head[w] = out[w]->head_stride;
-        op.vec = op.vec && heads_aligned(*in[w], elem, 16) && heads_aligned(*out[w], elem, 16);
+        aligned = aligned && heads_aligned(*in[w], elem, 16) && heads_aligned(*out[w], elem, 16);
     }
     if (keys && (a->q_out.data == a->k_out.data || a->q_out.data == a->k.data || a->k_out.data == a->q.data))
         return fail(JD_ERR_INVALID_ARG, "an output is the other output or the other input");
@@ -403,12 +777,11 @@ jd_status rotary_call(const jd_rotary_args *a, const jd_head_norm *norm, void *s
     op.head_dim = a->head_dim;
     op.dims = a->rotary.dims;
     op.interleaved = a->rotary.layout == JD_ROTARY_INTERLEAVED;
-    op.lanes_per_head = 1;
-    while (op.lanes_per_head * 8 < a->head_dim) op.lanes_per_head *= 2;
     op.positions = a->positions;
     op.cu = a->cu_seqlens;
     op.n_rows = a->n_rows;
     op.n_tokens = a->n_tokens;
+    rotary_plan(op, aligned);
     op.norm = norm != nullptr;
     if (norm) {
         op.layer_norm = norm->kind == JD_NORM_LAYER;

@@ -15,8 +15,11 @@ struct RotaryOp {
     int64_t src_token[2], src_head[2], dst_token[2], dst_head[2];
     int n_heads[2];
     int dtype, head_dim, dims;
-    int lanes_per_head;       // power of two >= head_dim / 8
-    bool interleaved, vec;    // vec: head_dim, pointers and strides allow 16-byte accesses
+    bool interleaved;
+    // set by rotary_plan: the kernel, and how a token's heads are laid over its threads
+    bool vec, vec8;
+    int lanes_per_head, heads_at_once;  // powers of two
+    int tokens_per_cta, ctas;
     bool in_place;            // both outputs are their inputs
     bool norm, layer_norm;
     const int *positions, *cu;  // positions, or row offsets [n_rows + 1]
@@ -25,6 +28,8 @@ struct RotaryOp {
     float eps, amplitude;
     double turns[ROTARY_MAX_PAIRS];
 };
+// Choose the kernel; `aligned`: pointers and strides (gains included) on multiples of 16 bytes.
+void rotary_plan(RotaryOp &op, bool aligned);
 cudaError_t launch_rotary(const RotaryOp &op, cudaStream_t st);
 
 }  // namespace jd

@@ -485,7 +485,7 @@ typedef struct {
 /* Queries and keys of n_tokens packed tokens.  Positions are positions[t]
  * where given (device, [n_tokens]; cu_seqlens is then not read), else the
  * token's index in its row, from cu_seqlens (device, [n_rows + 1], ascending
- * from 0): tokens past cu_seqlens[n_rows] are left alone, read or written.
+ * from 0): nothing is written for tokens past cu_seqlens[n_rows].
  * q_out / k_out may be q / k themselves (the same pointer and strides: in
  * place) or must not overlap any input or each other.  k.n_heads = 0: queries
  * only. */
