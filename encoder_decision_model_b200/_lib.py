@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from pathlib import Path
 
 import numpy as np
@@ -95,6 +96,15 @@ class jd_head_norm(C.Structure):
     _fields_ = [("kind", C.c_int32), ("eps", C.c_float), ("q_gain", C.c_void_p), ("k_gain", C.c_void_p)]
 
 
+class jd_diff_attention_args(C.Structure):
+    _fields_ = [("qk_dtype", C.c_int32), ("v_dtype", C.c_int32), ("n_tokens", C.c_int32), ("n_rows", C.c_int32),
+                ("kv_heads", C.c_int32), ("window", C.c_int32), ("cu_seqlens", C.c_void_p), ("q", jd_heads),
+                ("k", jd_heads), ("v", jd_heads), ("out", jd_heads), ("lambda_q1", C.c_void_p),
+                ("lambda_k1", C.c_void_p), ("lambda_q2", C.c_void_p), ("lambda_k2", C.c_void_p),
+                ("norm_gain", C.c_void_p), ("lambda_init", C.c_float), ("norm_eps", C.c_float), ("scale", C.c_float),
+                ("status", C.c_void_p)]
+
+
 # jd_route_scorer: (user, rows, n_rows, probs) -> jd_status
 ROUTE_SCORER = C.CFUNCTYPE(C.c_int, C.c_void_p, C.POINTER(jd_row), C.c_int32, C.POINTER(C.c_float))
 
@@ -161,9 +171,11 @@ def lib():
     L.jd_last_launch_count.restype = C.c_int32
     L.jd_set_profiling.argtypes = [C.c_void_p, C.c_int]
     L.jd_profile_report.argtypes = [C.c_void_p, C.c_char_p, C.c_size_t]
-    L.jd_rotary.argtypes = [C.POINTER(jd_rotary_args), C.c_void_p]
-    L.jd_qk_norm_rotary.argtypes = [C.POINTER(jd_rotary_args), C.POINTER(jd_head_norm), C.c_void_p]
-    for name in ("jd_rotary", "jd_qk_norm_rotary"):
+    # the operators' arguments: structures by reference, or their bytes
+    L.jd_rotary.argtypes = [C.c_void_p, C.c_void_p]
+    L.jd_qk_norm_rotary.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+    L.jd_diff_attention.argtypes = [C.c_void_p, C.c_void_p]
+    for name in ("jd_rotary", "jd_qk_norm_rotary", "jd_diff_attention"):
         getattr(L, name).restype = C.c_int
     for name in ("jd_serialize", "jd_model_create", "jd_model_create_shared", "jd_decide", "jd_forward", "jd_decide_host",
                  "jd_decide_packed_host", "jd_check_status", "jd_set_graph_mode", "jd_graph_stats", "jd_set_profiling",
@@ -404,7 +416,8 @@ def jd_route_scored(requests, score):
 
 # ---------------------------------------------------------------- operators
 
-_DTYPES = {"torch.float32": JD_F32, "torch.float16": JD_F16, "torch.bfloat16": JD_BF16}
+_NAMES = {"torch.float32": JD_F32, "torch.float16": JD_F16, "torch.bfloat16": JD_BF16, "torch.int32": "int32"}
+_KINDS = {}  # the same by dtype object, filled as dtypes are met
 _LAYOUTS = {"half": JD_ROTARY_HALF, "interleaved": JD_ROTARY_INTERLEAVED}
 _SCALINGS = {"none": JD_SCALING_NONE, "linear": JD_SCALING_LINEAR, "ntk": JD_SCALING_NTK, "yarn": JD_SCALING_YARN}
 _NORMS = {"rms": JD_NORM_RMS, "layer": JD_NORM_LAYER}
@@ -414,29 +427,37 @@ def _bad(msg):
     return JDError(JD_ERR_INVALID_ARG, msg)
 
 
+def _kind(dtype):
+    k = _KINDS.get(dtype)
+    if k is None:
+        k = _KINDS[dtype] = _NAMES.get(str(dtype), "other")
+    return k
+
+
 def _dtype(t):
-    try:
-        return _DTYPES[str(t.dtype)]
-    except KeyError:
-        raise _bad(f"unsupported dtype {t.dtype}") from None
+    k = _kind(t.dtype)
+    if k.__class__ is str:
+        raise _bad(f"unsupported dtype {t.dtype}")
+    return k
 
 
 def _heads(t, like=None):
-    """jd_heads of a [tokens, heads, head_dim] tensor; `like`: the (shape, dtype) it must have."""
+    """(data, token stride, head stride, heads) of a [tokens, heads, head_dim] tensor, the fields of jd_heads;
+    `like`: the (shape, dtype) it must have."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise _bad(f"a [tokens, heads, head_dim] tensor with contiguous heads is required, got {tuple(shape)}")
     if like is not None and (shape != like[0] or t.dtype != like[1]):
         raise _bad(f"a tensor is {tuple(shape)} {t.dtype}, not {tuple(like[0])} {like[1]}")
-    return jd_heads(t.data_ptr(), stride[0], stride[1], shape[1])
+    return t.data_ptr(), stride[0], stride[1], shape[1]
 
 
-def _vector(t, dtype, n, name):
-    """Pointer of a contiguous vector of n elements (None passes through)."""
+def _vector(t, kind, n, name):
+    """Pointer of a contiguous vector of n elements, 0 for None."""
     if t is None:
-        return None
-    if str(t.dtype) != dtype or t.numel() != n or not t.is_contiguous():
-        raise _bad(f"{name}: a contiguous {dtype} tensor of {n} elements is required")
+        return 0
+    if _kind(t.dtype) != kind or t.numel() != n or not t.is_contiguous():
+        raise _bad(f"{name}: a contiguous {'int32' if kind == 'int32' else 'float32'} tensor of {n} elements is required")
     return t.data_ptr()
 
 
@@ -450,38 +471,71 @@ def rotary_config(dims, theta, layout="half", scaling="none", factor=1.0, origin
         raise _bad(f"unknown rotary layout or scaling {e}") from None
 
 
+# The calls' arguments as bytes: packing them costs a third of filling the ctypes structures
+_HEADS = "Pqqi4x"
+_ROTARY_ARGS = struct.Struct("@iidiiddd" + "iiii" + "PP" + 4 * _HEADS)
+_HEAD_NORM = struct.Struct("@ifPP")
+_DIFF_ARGS = struct.Struct("@iiiiiiP" + 4 * _HEADS + "PPPPPfff4xP")
+
+
 def _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions):
+    """(jd_rotary_args as bytes, head_dim)"""
     hq = _heads(q)
-    T, _, d = q.shape
+    shape, dtype = q.shape, q.dtype
+    T, _, d = shape
     if k is None:
-        hk = hko = jd_heads()
+        hk = hko = (0, 0, 0, 0)
     else:
         hk = _heads(k)
-        if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or k_out is None:
+        ks = k.shape
+        if ks[0] != T or ks[2] != d or k.dtype != dtype or k_out is None:
             raise _bad("k must have q's tokens, head_dim and dtype, and an output")
-        hko = _heads(k_out, (k.shape, k.dtype))
+        hko = _heads(k_out, (ks, dtype))
     n_rows = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    return jd_rotary_args(rotary, _dtype(q), d, T, n_rows, _vector(positions, "torch.int32", T, "positions"),
-                          _vector(cu_seqlens, "torch.int32", n_rows + 1, "cu_seqlens"), hq, hk,
-                          _heads(q_out, (q.shape, q.dtype)), hko)
+    r = rotary
+    return _ROTARY_ARGS.pack(r.layout, r.dims, r.theta, r.scaling, r.original_length, r.factor, r.beta_fast,
+                             r.beta_slow, _dtype(q), d, T, n_rows, _vector(positions, "int32", T, "positions"),
+                             _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"), *hq, *hk,
+                             *_heads(q_out, (shape, dtype)), *hko), d
 
 
 def jd_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=None, positions=None, stream=None):
     """Rotate q and k (device tensors [tokens, heads, head_dim]; k may be None) into q_out and k_out, which may be
     q and k themselves.  Positions: `positions` (int32 per token), else the index in the row from `cu_seqlens`."""
-    a = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
-    _check(lib().jd_rotary(C.byref(a), _stream(stream)))
+    a, _ = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
+    _check(lib().jd_rotary(a, _stream(stream)))
 
 
 def jd_qk_norm_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=None, positions=None, norm="rms",
                       eps=1e-5, q_gain=None, k_gain=None, stream=None):
     """jd_rotary with a norm ("rms" or "layer", gains float32 [head_dim] or None) of every head before the rotation."""
-    a = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
+    a, d = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
     if norm not in _NORMS:
         raise _bad(f"unknown norm {norm!r}")
-    n = jd_head_norm(_NORMS[norm], eps, _vector(q_gain, "torch.float32", a.head_dim, "q_gain"),
-                     _vector(k_gain, "torch.float32", a.head_dim, "k_gain"))
-    _check(lib().jd_qk_norm_rotary(C.byref(a), C.byref(n), _stream(stream)))
+    n = _HEAD_NORM.pack(_NORMS[norm], eps, _vector(q_gain, JD_F32, d, "q_gain"), _vector(k_gain, JD_F32, d, "k_gain"))
+    _check(lib().jd_qk_norm_rotary(a, n, _stream(stream)))
+
+
+def jd_diff_attention(q, k, v, out, cu_seqlens, lambda_q1, lambda_k1, lambda_q2, lambda_k2, lambda_init, norm_gain=None,
+                      norm_eps=1e-5, window=-1, scale=0.0, status=None, stream=None):
+    """Differential attention inside each packed row.  q [tokens, 2 heads, 64], k [tokens, 2 kv_heads, 64], v [tokens,
+    kv_heads, 128], out [tokens, heads, 128]; the lambda vectors (64) and norm_gain (128) are float32; window < 0 for
+    the whole row; status: an int32 device tensor that collects failed checks, or None."""
+    hq, hk, hv, ho = _heads(q), _heads(k), _heads(v), _heads(out)
+    T, dtype, kv = q.shape[0], q.dtype, hv[3]
+    if k.dtype != dtype or out.dtype != dtype:
+        raise _bad("q, k and out must have one dtype")
+    if k.shape[0] != T or v.shape[0] != T or out.shape[0] != T:
+        raise _bad("q, k, v and out must have the same tokens")
+    if q.shape[2] != 64 or k.shape[2] != 64 or v.shape[2] != 128 or out.shape[2] != 128:
+        raise _bad("query and key heads are 64 wide, values and outputs 128")
+    n_rows = cu_seqlens.numel() - 1
+    a = _DIFF_ARGS.pack(_dtype(q), _dtype(v), T, n_rows, kv, window, _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"),
+                        *hq, *hk, *hv, *ho, _vector(lambda_q1, JD_F32, 64, "lambda_q1"),
+                        _vector(lambda_k1, JD_F32, 64, "lambda_k1"), _vector(lambda_q2, JD_F32, 64, "lambda_q2"),
+                        _vector(lambda_k2, JD_F32, 64, "lambda_k2"), _vector(norm_gain, JD_F32, 128, "norm_gain"),
+                        lambda_init, norm_eps, scale, _vector(status, "int32", 1, "status"))
+    _check(lib().jd_diff_attention(a, _stream(stream)))
 
 
 class Model:

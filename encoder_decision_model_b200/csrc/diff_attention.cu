@@ -1,0 +1,817 @@
+// Differential attention over packed rows: D = softmax(Q0 K0^T) V - lambda softmax(Q1 K1^T) V, with
+// each head's RMS norm and gain in the same launch.
+//
+// One pass over the keys with the running maximum and sum of both softmaxes.  A work item is 128
+// queries of one row and head; its two maps run side by side, as two query tiles of an ordinary
+// attention would, over the same 128-wide V tiles:
+//
+//   warp 0          TMA producer of the item's Q_0, Q_1 (two buffers) and of K_0, K_1 tiles (a ring of
+//                   16 KB units, freed when their S product completes)
+//   warp 2          TMA producer of V tiles (128 keys x 128, a ring of 32 KB stages)
+//   warp 3          zeroes the rows of an item's last V tile that lie past its keys: their
+//                   probabilities are 0, but 0 times what another row holds there may be NaN
+//   warp 1          TMEM; lane 0 issues tcgen05.mma:
+//                     S_x = Q_x K_x^T  (M 128, N 128, K 64)
+//                     O_x += P_x V     (M 128, N 128, K 128; P from TMEM, V read MN-major)
+//   warps 4..7      softmax of map 0, warps 8..11 of map 1: one query row a thread
+//
+// TMEM is full: S_0, S_1 in columns 0..255, O_0, O_1 in 256..511.  P_x overwrites S_x (the thread
+// that stores a row's P has read all of its S), so S_x of the next tile waits for this tile's
+// P_x V; meanwhile the other map's group has the special-function unit.  At an item's end both
+// groups hold the same queries: group x reads columns 64 x .. 64 x + 63 of O_0 and O_1, forms D,
+// and the two halves of a row's sum of squares meet in shared memory.
+//
+// Bound: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
+// exponentials a clock and SM, 0.094 and 0.125 clocks.
+//
+// Rounding of P.  P enters the PV product in 16 bits.  With FP16 values and a BF16 result P in FP16
+// (2^-12) disappears behind the result's 2^-9.  Otherwise P's rounding would be as large as the
+// result's own and, since D is a difference, up to (1 + lambda) / (1 - lambda) times larger after
+// the norm: there P goes in as a pair hi + lo (lo in S's other 64 columns), twice the MMAs of PV.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cmath>
+#include <mutex>
+
+#include "common.cuh"
+#include "diff_attention.h"
+#include "kernels.h"
+
+namespace jd {
+
+namespace {
+
+constexpr int TQ = 128, TK = 128, VD = 128;
+constexpr int Q_BYTES = TQ * 128;            // one map's queries: 128 rows x 64 elements of 16 bits
+constexpr int K_BYTES = TK * 128;            // one map's keys
+constexpr int V_HALF = TK * 128;             // 64 columns of a V tile
+constexpr int V_BYTES = 2 * V_HALF;
+constexpr int NK = 4, NV = 2;                // ring depths
+constexpr int OFF_Q = 0;                     // [item buffer][map]
+constexpr int OFF_K = OFF_Q + 4 * Q_BYTES;
+constexpr int OFF_V = OFF_K + NK * K_BYTES;
+constexpr int OFF_BAR = OFF_V + NV * V_BYTES;
+constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 2 + 1;
+constexpr int OFF_F = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;
+// floats: gain[128], l[2][128], sums of squares[2][128], lambda; then the TMEM slot and a status word
+constexpr int DIFF_SMEM = OFF_F + (128 + 256 + 256 + 4) * 4 + 16 + 1024;
+static_assert(DIFF_SMEM <= 227 * 1024, "differential attention shared memory");
+constexpr uint32_t T_S = 0, T_O = 256;
+constexpr float kLazy = 8.0f;                // log2 headroom before a running max is moved: P <= 2^8
+constexpr int THREADS = 12 * 32;
+// As in the global attention: the compiled count (checked on the host), what warp group 0 keeps and
+// what each softmax group takes.
+constexpr int REGS = 168, REGS_LOW = 120, REGS_HIGH = 192;
+static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= THREADS * REGS, "register split");
+constexpr int BAR_SUMS = 1, BAR_SQUARES = 2;  // named barriers of the two softmax groups
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_heads(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int head, int token) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(token)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16: A is 128 x 16 in TMEM (lane = row, two elements a column)
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// MN-major tile with 128-byte swizzle: rows of 64 elements, eight keys 1024 bytes apart (stride), the
+// next 64 elements V_HALF further on (leading).
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(V_HALF >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+struct Item {
+    int h, cs, ce, q0;   // head, row, first query
+    int k0, kend, nt;    // keys [k0, kend) in nt tiles
+    bool on;
+    __device__ int in_last() const { return kend - k0 - (nt - 1) * TK; }  // keys of the last tile
+};
+
+// Work item w: head w % heads of query tile w / heads.  Tile numbers are spread so that no table is
+// needed: row r's tiles start at cu[r] / 128 + r, which leaves every row room for all of its tiles; a
+// number past a row's last tile is an empty item.  The row is found 32 probes at a time; all lanes
+// of a warp call this.
+__device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
+    Item t;
+    const int b = w / p.heads;
+    t.h = w - b * p.heads;
+    int lo = 0, n = p.n_rows;
+    t.on = true;
+    while (n > 1) {
+        const int step = (n + 31) >> 5, at = lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < n && (p.cu[lo + at] >> 7) + lo + at <= b);
+        if (!(below & 1u)) {
+            t.on = false;
+            break;
+        }
+        const int k = 31 - __clz(below);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    t.cs = max(p.cu[lo], 0);
+    t.ce = min(p.cu[lo + 1], p.n_tokens);
+    t.q0 = t.cs + (b - (t.cs >> 7) - lo) * TQ;
+    t.on = t.on && t.q0 >= t.cs && t.q0 < t.ce;
+    t.k0 = p.window < 0 ? t.cs : max(t.cs, t.q0 - p.window);
+    t.kend = p.window < 0 ? t.ce : min(t.ce, min(t.q0 + TQ, t.ce) + p.window);
+    t.nt = (t.kend - t.k0 + TK - 1) / TK;
+    return t;
+}
+
+template <bool V16>  // V16: FP16 values, else BF16
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+    return V16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+template <bool V16>
+__device__ __forceinline__ float2 unpack_p(uint32_t u) {
+    if (V16) return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// V16: FP16 values; SPLIT: P as hi + lo
+template <bool V16, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_diff_attention(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DiffOp p, int n_items) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+    uint64_t *qfull = bars, *qfree = qfull + 2, *kfull = qfree + 2, *kfree = kfull + NK, *vfull = kfree + NK,
+             *vfree = vfull + NV, *vtail = vfree + NV, *sfull = vtail + NV, *pready = sfull + 2, *pvdone = pready + 2,
+             *ofree = pvdone + 2;
+    float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128, *squares = sums + 256,
+          *lambda = squares + 256;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lambda + 4);
+    unsigned *own_status = tmem_slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&kfull[i], 1);
+            mbar_init(&kfree[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&vfull[i], 1);
+            mbar_init(&vfree[i], 1);
+            mbar_init(&vtail[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qfree[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pready[i], 4);
+            mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(ofree, 8);
+        *own_status = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 3) {
+        const float a = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
+        const float b = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
+        if (lane == 0) *lambda = expf(a) - expf(b) + p.lambda_init;
+        for (int i = lane; i < 128; i += 32) gain[i] = p.gain ? p.gain[i] * (1.0f - p.lambda_init) : 1.0f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    unsigned *status = p.status ? p.status : own_status;
+    if (warp < 4) {  // warp group 0: producers, MMA issue, the tail of V
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW));
+        if (warp == 0) {
+            uint32_t U = 0, it = 0;
+            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+                const Item t = find_item(p, w, lane);
+                if (!t.on) continue;
+                if (lane == 0) {
+                    const int kh = 2 * (t.h / (p.heads / p.kv_heads));
+                    const uint32_t buf = it & 1;
+                    if (it >= 2) mbar_wait(&qfree[buf], ((it - 2) >> 1) & 1, status);
+                    mbar_arrive_expect_tx(&qfull[buf], 2 * Q_BYTES);
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_heads(smem + OFF_Q + (buf * 2 + x) * Q_BYTES, &tm_q, &qfull[buf], 0, 2 * t.h + x, t.q0);
+                    for (int j = 0; j < t.nt; ++j)
+                        for (int x = 0; x < 2; ++x, ++U) {
+                            const uint32_t s = U % NK;
+                            if (U >= NK) mbar_wait(&kfree[s], ((U - NK) / NK) & 1, status);
+                            mbar_arrive_expect_tx(&kfull[s], K_BYTES);
+                            tma_load_heads(smem + OFF_K + s * K_BYTES, &tm_k, &kfull[s], 0, kh + x, t.k0 + j * TK);
+                        }
+                }
+                ++it;
+                __syncwarp();
+            }
+        } else if (warp == 2) {
+            uint32_t J = 0;
+            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+                const Item t = find_item(p, w, lane);
+                if (!t.on) continue;
+                if (lane == 0) {
+                    const int vh = t.h / (p.heads / p.kv_heads);
+                    for (int j = 0; j < t.nt; ++j, ++J) {
+                        const uint32_t s = J % NV;
+                        if (J >= NV) mbar_wait(&vfree[s], ((J - NV) / NV) & 1, status);
+                        // a tile that warp 3 has to finish lands on a barrier of its own
+                        uint64_t *bar = j == t.nt - 1 && (t.in_last() & 15) ? &vtail[s] : &vfull[s];
+                        mbar_arrive_expect_tx(bar, V_BYTES);
+                        for (int x = 0; x < 2; ++x)
+                            tma_load_heads(smem + OFF_V + s * V_BYTES + x * V_HALF, &tm_v, bar, 64 * x, vh,
+                                           t.k0 + j * TK);
+                    }
+                }
+                __syncwarp();
+            }
+        } else if (warp == 3) {
+            uint32_t J = 0, tails[NV] = {};
+            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+                const Item t = find_item(p, w, lane);
+                if (!t.on) continue;
+                J += t.nt;
+                const int valid = t.in_last();
+                if ((valid & 15) == 0) continue;  // the MMAs stop at the last whole step of 16 keys
+                const uint32_t s = (J - 1) % NV;
+                mbar_wait(&vtail[s], tails[s]++ & 1, status);
+                const int pieces = (((valid + 15) & ~15) - valid) * 8;  // 16 bytes each, in both halves
+                for (int i = lane; i < 2 * pieces; i += 32) {
+                    uint8_t *half = smem + OFF_V + s * V_BYTES + (i >= pieces ? V_HALF : 0);
+                    *reinterpret_cast<uint4 *>(half + valid * 128 + (i >= pieces ? i - pieces : i) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&vfull[s]);
+            }
+        } else {
+            const uint32_t qk16 = p.qk_dtype == JD_F16;
+            const uint32_t idesc_s = qk16 ? idesc_f16_f32(TK) : idesc_bf16_f32(TK);
+            const uint32_t idesc_pv = (V16 ? idesc_f16_f32(VD) : idesc_bf16_f32(VD)) | (1u << 16);  // V is MN-major
+            uint32_t U = 0, J = 0, it = 0;
+            uint32_t n_pv[2] = {0, 0};
+            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+                const Item t = find_item(p, w, lane);
+                if (!t.on) continue;
+                if (lane == 0) {
+                    const uint32_t buf = it & 1;
+                    mbar_wait(&qfull[buf], (it >> 1) & 1, status);
+                    // S_x of tile j: K_x is unit U + 2 j + x; the last P_x must have been used
+                    auto issue_s = [&](int j, int x) {
+                        const uint32_t u = U + 2 * j + x, s = u % NK;
+                        mbar_wait(&kfull[s], (u / NK) & 1, status);
+                        if (n_pv[x]) mbar_wait(&pvdone[x], (n_pv[x] - 1) & 1, status);
+                        tc_fence_after();
+                        const uint32_t q = smem_u32(smem + OFF_Q + (buf * 2 + x) * Q_BYTES);
+                        const uint32_t k = smem_u32(smem + OFF_K + s * K_BYTES);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(tmem + T_S + TK * x, sdesc_sw128(q + kk * 32), sdesc_sw128(k + kk * 32), idesc_s,
+                                        kk != 0);
+                        tc_commit(&sfull[x]);
+                        tc_commit(&kfree[s]);
+                        if (x == 1 && j == t.nt - 1) tc_commit(&qfree[buf]);
+                    };
+                    issue_s(0, 0);
+                    issue_s(0, 1);
+                    const int valid = t.in_last();
+                    for (int j = 0; j < t.nt; ++j, ++J) {
+                        const uint32_t s = J % NV;
+                        const bool last = j == t.nt - 1;
+                        mbar_wait(&vfull[s], (J / NV) & 1, status);
+                        const int steps = last ? (valid + 15) >> 4 : TK / 16;
+                        const uint32_t v = smem_u32(smem + OFF_V + s * V_BYTES);
+                        for (int x = 0; x < 2; ++x) {
+                            mbar_wait(&pready[x], n_pv[x] & 1, status);
+                            if (j == 0 && x == 0 && it > 0) mbar_wait(ofree, (it - 1) & 1, status);
+                            tc_fence_after();
+                            for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+                                for (int ks = 0; ks < steps; ++ks)
+                                    mma_ts(tmem + T_O + VD * x, tmem + T_S + TK * x + 64 * part + 8 * ks,
+                                           sdesc_v(v + ks * 16 * 128), idesc_pv, j != 0 || ks != 0 || part != 0);
+                            tc_commit(&pvdone[x]);
+                            ++n_pv[x];
+                            if (x == 1) tc_commit(&vfree[s]);
+                            if (!last) issue_s(j + 1, x);
+                        }
+                    }
+                    U += 2 * t.nt;
+                }
+                ++it;
+                __syncwarp();
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_HIGH));
+        const int x = (warp - 4) >> 2;         // this group's map
+        const int r = (warp & 3) * 32 + lane;  // query row inside the tile = TMEM lane
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = tl + T_S + TK * x, to = tl + T_O;
+        const float sl2 = p.scale * 1.4426950408889634f;
+        const float lam = *lambda;
+        uint32_t c = 0;  // tiles of this map so far
+        for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
+            const Item t = find_item(p, w, lane);
+            if (!t.on) continue;
+            const int qi = t.q0 + r;
+            const bool dead = t.q0 + (warp & 3) * 32 >= t.ce;  // no row of this warp: it only keeps the order
+            // keys this row sees: [lo, hi)
+            const int lo = p.window < 0 ? t.cs : max(t.cs, qi - p.window);
+            const int hi = p.window < 0 ? t.ce : min(t.ce, qi + p.window + 1);
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < t.nt; ++j, ++c) {
+                mbar_wait(&sfull[x], c & 1, status);
+                __syncwarp();
+                if (!dead) {
+                    tc_fence_after();
+                    uint32_t sv[128];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tmem_ld32(ts + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
+                    tmem_ld_wait();
+                    const int a = lo - (t.k0 + j * TK), b = hi - (t.k0 + j * TK);
+                    if (__any_sync(0xffffffffu, a > 0 || b < TK)) {
+#pragma unroll
+                        for (int e = 0; e < TK; ++e)
+                            if (e < a || e >= b) sv[e] = __float_as_uint(-INFINITY);
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m4[i] = fmaxf(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+#pragma unroll
+                    for (int e = 8; e < TK; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            m4[i] = max3(m4[i], __uint_as_float(sv[e + 2 * i]), __uint_as_float(sv[e + 2 * i + 1]));
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+                    // Rows move their maximum one by one, but TMEM is read and written by whole warps (the
+                    // instructions are aligned): all rows of the warp go along, most with a factor of 1.
+                    // S_x being there, every earlier PV_x has landed.
+                    const bool grows = mx > m + kLazy, scaled = grows && m != -INFINITY;
+                    if (__any_sync(0xffffffffu, scaled)) {
+                        const float alpha = scaled ? exp2_fast(m - mx) : 1.0f;
+                        l *= alpha;
+#pragma unroll 1
+                        for (int hc = 0; hc < VD; hc += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + VD * x + hc, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(to + VD * x + hc, o);
+                        }
+                    }
+                    if (grows) m = mx;
+                    __syncwarp();
+                    const float mm = m == -INFINITY ? 0.f : m;  // nothing seen yet: every P is 0
+                    float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                    for (int hk = 0; hk < 2; ++hk) {
+                        uint32_t pk[32], pl[SPLIT ? 32 : 1];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 xv = fma_f32x2(
+                                make_float2(__uint_as_float(sv[64 * hk + e]), __uint_as_float(sv[64 * hk + e + 1])),
+                                make_float2(sl2, sl2), make_float2(-mm, -mm));
+                            const float p0 = exp2_fast(xv.x), p1 = exp2_fast(xv.y);
+                            ls[(e >> 1) & 3] = add_f32x2(ls[(e >> 1) & 3], make_float2(p0, p1));
+                            pk[e >> 1] = pack_p<V16>(p0, p1);
+                            if (SPLIT) {
+                                const float2 h = unpack_p<V16>(pk[e >> 1]);
+                                pl[e >> 1] = pack_p<V16>(p0 - h.x, p1 - h.y);
+                            }
+                        }
+                        tmem_st32(ts + 32 * hk, pk);
+                        if constexpr (SPLIT) tmem_st32(ts + 64 + 32 * hk, pl);
+                    }
+                    l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[x]);
+            }
+            // Both maps' sums, then this group's half of the columns of both O
+            sums[128 * x + r] = l;
+            mbar_wait(&pvdone[0], (c - 1) & 1, status);
+            mbar_wait(&pvdone[1], (c - 1) & 1, status);
+            __syncwarp();
+            named_bar_sync(BAR_SUMS, 256);
+            float d[64], sq = 0.f;
+            if (!dead) {
+                tc_fence_after();
+                const float i0 = 1.0f / sums[r], i1 = -lam / sums[128 + r];
+#pragma unroll
+                for (int hc = 0; hc < 64; hc += 32) {
+                    uint32_t o0[32], o1[32];
+                    tmem_ld32(to + 64 * x + hc, o0);
+                    tmem_ld32(to + VD + 64 * x + hc, o1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        d[hc + e] = fmaf(__uint_as_float(o1[e]), i1, __uint_as_float(o0[e]) * i0);
+                        sq = fmaf(d[hc + e], d[hc + e], sq);
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofree);
+            squares[128 * x + r] = sq;
+            __syncwarp();
+            named_bar_sync(BAR_SQUARES, 256);
+            if (qi < t.ce) {
+                const float f = p.gain ? rsqrtf((squares[r] + squares[128 + r]) * (1.0f / VD) + p.eps) : 1.0f;
+                uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (qi * p.out_token + t.h * p.out_head + 64 * x);
+                const bool out16 = p.qk_dtype == JD_F16;
+#pragma unroll
+                for (int e = 0; e < 64; e += 8) {
+                    const float4 g0 = *reinterpret_cast<const float4 *>(&gain[64 * x + e]),
+                                 g1 = *reinterpret_cast<const float4 *>(&gain[64 * x + e + 4]);
+                    const float y[8] = {d[e] * f * g0.x,     d[e + 1] * f * g0.y, d[e + 2] * f * g0.z, d[e + 3] * f * g0.w,
+                                        d[e + 4] * f * g1.x, d[e + 5] * f * g1.y, d[e + 6] * f * g1.z, d[e + 7] * f * g1.w};
+                    uint32_t u[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        u[i] = out16 ? pack_f16x2(y[2 * i], y[2 * i + 1]) : pack_bf16x2(y[2 * i], y[2 * i + 1]);
+                    *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ FP32
+
+constexpr int FQ = 64, FK = 64, FP = 68;  // queries and keys of a tile; padded row of a transposed tile
+constexpr int F32_SMEM = (2 * 64 * FP * 2 + FK * VD + 2 * FK * FP + 128 + 4) * 4;
+
+// 64 queries of one row and head, all of its keys in tiles of 64; a thread holds 4 x 4 scores of each
+// map and 4 x 8 outputs of each.  Tiles lie transposed (element-major) in shared memory, so that a
+// product step reads whole vectors.
+__global__ void __launch_bounds__(256) k_diff_attention_f32(const __grid_constant__ DiffOp p) {
+    extern __shared__ float fs[];
+    float *Q = fs, *K = Q + 2 * 64 * FP, *V = K + 2 * 64 * FP, *P = V + FK * VD, *gain = P + 2 * FK * FP,
+          *lambda = gain + 128;
+    const int tid = threadIdx.x, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
+    // the tiles' numbering of find_item, with 64 queries a tile
+    const int b = blockIdx.x, h = blockIdx.y;
+    int row = 0, n = p.n_rows;
+    while (n > 1) {
+        const int step = (n + 31) >> 5, at = lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < n && (p.cu[row + at] >> 6) + row + at <= b);
+        if (!(below & 1u)) return;
+        const int k = 31 - __clz(below);
+        row += k * step;
+        n = min(step, n - k * step);
+    }
+    const int cs = max(p.cu[row], 0), ce = min(p.cu[row + 1], p.n_tokens);
+    const int q0 = cs + (b - (cs >> 6) - row) * FQ;
+    if (q0 < cs || q0 >= ce) return;
+    const int k0 = p.window < 0 ? cs : max(cs, q0 - p.window);
+    const int kend = p.window < 0 ? ce : min(ce, min(q0 + FQ, ce) + p.window);
+    const int g = h / (p.heads / p.kv_heads);
+    const float *qp = static_cast<const float *>(p.q) + 2 * h * p.q_head;
+    const float *kp = static_cast<const float *>(p.k) + 2 * g * p.k_head;
+    const float *vp = static_cast<const float *>(p.v) + g * p.v_head;
+    if (tid < 32) {
+        const float a = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
+        const float c = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
+        if (lane == 0) *lambda = expf(a) - expf(c) + p.lambda_init;
+    }
+    if (tid < 128) gain[tid] = p.gain ? p.gain[tid] * (1.0f - p.lambda_init) : 1.0f;
+    auto load_t = [&](float *dst, const float *src, int64_t token, int64_t head, int first, int end) {
+        // two maps x 64 rows x 16 vectors: neighbouring threads take neighbouring rows
+        for (int i = tid; i < 2 * 64 * 16; i += 256) {
+            const int r = i & 63, v4 = (i >> 6) & 15, m = i >> 10;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (first + r < end) a = *reinterpret_cast<const float4 *>(src + (first + r) * token + m * head + 4 * v4);
+            float *d = dst + (m * 64 + 4 * v4) * FP + r;
+            d[0] = a.x, d[FP] = a.y, d[2 * FP] = a.z, d[3 * FP] = a.w;
+        }
+    };
+    load_t(Q, qp, p.q_token, p.q_head, q0, ce);
+    float o[2][4][8], m[2][4], l[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[x][i] = -INFINITY, l[x][i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[x][i][e] = 0.f;
+        }
+    for (int kt = k0; kt < kend; kt += FK) {
+        __syncthreads();  // the last tile's K, V and P have been used
+        load_t(K, kp, p.k_token, p.k_head, kt, kend);
+        for (int i = tid; i < FK * VD / 4; i += 256) {
+            const int r = i >> 5, v4 = i & 31;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (kt + r < kend) a = *reinterpret_cast<const float4 *>(vp + (kt + r) * p.v_token + 4 * v4);
+            *reinterpret_cast<float4 *>(V + r * VD + 4 * v4) = a;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float s[4][4] = {};
+#pragma unroll 8
+            for (int d = 0; d < 64; ++d) {
+                const float4 a = *reinterpret_cast<const float4 *>(Q + (x * 64 + d) * FP + 4 * ty);
+                const float4 c = *reinterpret_cast<const float4 *>(K + (x * 64 + d) * FP + 4 * tx);
+                const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][e] = fmaf(av[i], cv[e], s[i][e]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int qi = q0 + 4 * ty + i;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kj = kt + 4 * tx + e;
+                    const bool seen = kj < kend && (p.window < 0 || (kj - qi <= p.window && qi - kj <= p.window));
+                    s[i][e] = seen ? s[i][e] * p.scale : -INFINITY;
+                    mx = fmaxf(mx, s[i][e]);
+                }
+                for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                const float now = fmaxf(m[x][i], mx), mm = now == -INFINITY ? 0.f : now;
+                const float alpha = expf(m[x][i] - mm);
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[i][e] = expf(s[i][e] - mm);
+                    sum += s[i][e];
+                }
+                l[x][i] = l[x][i] * alpha + sum;
+                m[x][i] = now;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[x][i][e] *= alpha;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4 *>(P + (x * FK + 4 * tx + e) * FP + 4 * ty) =
+                    make_float4(s[0][e], s[1][e], s[2][e], s[3][e]);
+        }
+        __syncthreads();
+        const int keys = min(FK, kend - kt);
+        for (int k = 0; k < keys; ++k) {
+            const float4 v0 = *reinterpret_cast<const float4 *>(V + k * VD + 4 * tx);
+            const float4 v1 = *reinterpret_cast<const float4 *>(V + k * VD + 64 + 4 * tx);
+            const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 a = *reinterpret_cast<const float4 *>(P + (x * FK + k) * FP + 4 * ty);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[x][i][e] = fmaf(av[i], vv[e], o[x][i][e]);
+            }
+        }
+    }
+    const float lam = *lambda;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float l0 = l[0][i], l1 = l[1][i];
+        for (int w = 8; w; w >>= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+        }
+        const float i0 = 1.0f / l0, i1 = -lam / l1;
+        float d[8], sq = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            d[e] = fmaf(o[1][i][e], i1, o[0][i][e] * i0);
+            sq = fmaf(d[e], d[e], sq);
+        }
+        for (int w = 8; w; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
+        const float f = p.gain ? 1.0f / sqrtf(sq * (1.0f / VD) + p.eps) : 1.0f;
+        const int qi = q0 + 4 * ty + i;
+        if (qi < ce) {
+            float *dst = static_cast<float *>(p.out) + qi * p.out_token + h * p.out_head;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = 64 * u + 4 * tx;
+                *reinterpret_cast<float4 *>(dst + at) =
+                    make_float4(d[4 * u] * f * gain[at], d[4 * u + 1] * f * gain[at + 1], d[4 * u + 2] * f * gain[at + 2],
+                                d[4 * u + 3] * f * gain[at + 3]);
+            }
+        }
+    }
+}
+
+const void *tensor_kernel(const DiffOp &op) {
+    const bool v16 = op.v_dtype == JD_F16, split = !(v16 && op.qk_dtype == JD_BF16);
+    if (!v16) return reinterpret_cast<const void *>(&k_diff_attention<false, true>);
+    return split ? reinterpret_cast<const void *>(&k_diff_attention<true, true>)
+                 : reinterpret_cast<const void *>(&k_diff_attention<true, false>);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(f);
+    });
+    return fn;
+}
+
+}  // namespace
+
+jd_status make_diff_maps(const DiffOp &op, DiffMaps *maps) {
+    EncodeTiled fn = encode_tiled();
+    if (!fn) return fail(JD_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    struct {
+        CUtensorMap *m;
+        const void *data;
+        int width, heads, dtype;
+        int64_t token, head;
+    } t[3] = {{&maps->q, op.q, 64, 2 * op.heads, op.qk_dtype, op.q_token, op.q_head},
+              {&maps->k, op.k, 64, 2 * op.kv_heads, op.qk_dtype, op.k_token, op.k_head},
+              {&maps->v, op.v, 128, op.kv_heads, op.v_dtype, op.v_token, op.v_head}};
+    for (auto &a : t) {
+        // an axis of one entry is never stepped along: any stride does
+        const cuuint64_t dims[3] = {(cuuint64_t)a.width, (cuuint64_t)a.heads, (cuuint64_t)op.n_tokens};
+        const cuuint64_t strides[2] = {2 * (cuuint64_t)(a.heads > 1 ? a.head : a.width),
+                                       2 * (cuuint64_t)(op.n_tokens > 1 ? a.token : a.width)};
+        const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+        const CUresult r =
+            fn(a.m, a.dtype == JD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(a.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(JD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    }
+    return JD_OK;
+}
+
+cudaError_t diff_attention_prepare(int device) {
+    static std::atomic<bool> done[64];
+    if (device >= 0 && device < 64 && done[device].load(std::memory_order_acquire)) return cudaSuccess;
+    const void *kernels[3] = {reinterpret_cast<const void *>(&k_diff_attention<false, true>),
+                              reinterpret_cast<const void *>(&k_diff_attention<true, true>),
+                              reinterpret_cast<const void *>(&k_diff_attention<true, false>)};
+    for (const void *k : kernels) {
+        // a group asking for more registers than the launch holds would wait for ever
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, k);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != REGS) return cudaErrorInvalidKernelImage;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, DIFF_SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_diff_attention_f32, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
+    if (e == cudaSuccess && device >= 0 && device < 64) done[device].store(true, std::memory_order_release);
+    return e;
+}
+
+cudaError_t launch_diff_attention(const DiffOp &op, const DiffMaps *maps, int num_sms, cudaStream_t st) {
+    if (op.n_tokens <= 0 || op.n_rows <= 0) return cudaSuccess;
+    if (op.qk_dtype == JD_F32) {
+        const dim3 grid(op.n_tokens / FQ + op.n_rows, op.heads);
+        k_diff_attention_f32<<<grid, 256, F32_SMEM, st>>>(op);
+        return cudaGetLastError();
+    }
+    const int64_t items = ((int64_t)op.n_tokens / TQ + op.n_rows) * op.heads;
+    int n_items = (int)items;
+    const int grid = n_items < num_sms ? n_items : num_sms;
+    void *args[5] = {const_cast<CUtensorMap *>(&maps->q), const_cast<CUtensorMap *>(&maps->k),
+                     const_cast<CUtensorMap *>(&maps->v), const_cast<DiffOp *>(&op), &n_items};
+    return cudaLaunchKernel(tensor_kernel(op), dim3(grid), dim3(THREADS), args, DIFF_SMEM, st);
+}
+
+}  // namespace jd
+
+using namespace jd;
+
+extern "C" jd_status jd_diff_attention(const jd_diff_attention_args *a, void *stream) {
+    clear_error();
+    if (!a) return fail(JD_ERR_INVALID_ARG, "NULL argument");
+    const bool f32 = a->qk_dtype == JD_F32;
+    if (a->qk_dtype != JD_F32 && a->qk_dtype != JD_F16 && a->qk_dtype != JD_BF16)
+        return fail(JD_ERR_INVALID_ARG, "unknown dtype %d", a->qk_dtype);
+    if (f32 ? a->v_dtype != JD_F32 : (a->v_dtype != JD_F16 && a->v_dtype != JD_BF16))
+        return fail(JD_ERR_INVALID_ARG, "v_dtype %d does not go with qk_dtype %d", a->v_dtype, a->qk_dtype);
+    if (a->n_tokens < 0 || a->n_rows < 0) return fail(JD_ERR_INVALID_ARG, "negative n_tokens or n_rows");
+    const int heads = a->out.n_heads, kv = a->kv_heads;
+    if (heads < 1 || heads > 32767 || kv < 1 || heads % kv)
+        return fail(JD_ERR_INVALID_ARG, "heads: out.n_heads 1..32767, a multiple of kv_heads");
+    if (a->q.n_heads != 2 * heads || a->k.n_heads != 2 * kv || a->v.n_heads != kv)
+        return fail(JD_ERR_INVALID_ARG, "heads: q has 2 heads, k 2 kv_heads, v kv_heads");
+    if (a->n_tokens > (1 << 30) || ((int64_t)a->n_tokens / 64 + a->n_rows) * heads > INT32_MAX - 65536)
+        return fail(JD_ERR_INVALID_ARG, "too many tokens, rows and heads");
+    if (!std::isfinite(a->lambda_init) || !(a->norm_eps >= 0) || !std::isfinite(a->norm_eps) || !(a->scale >= 0) ||
+        !std::isfinite(a->scale))
+        return fail(JD_ERR_INVALID_ARG, "lambda_init, norm_eps or scale is not finite, or norm_eps or scale negative");
+    const jd_heads *in[3] = {&a->q, &a->k, &a->v};
+    const char *name[3] = {"q", "k", "v"};
+    const size_t elem = f32 ? 4 : 2;
+    for (int i = 0; i < 3; ++i) {
+        const jd_heads &t = *in[i];
+        const int64_t most = (int64_t)1 << 38;  // a tensor map's strides are below 2^40 bytes
+        if ((t.token_stride < 1 && a->n_tokens > 1) || (t.head_stride < 1 && t.n_heads > 1) || t.token_stride > most ||
+            t.head_stride > most)
+            return fail(JD_ERR_INVALID_ARG, "%s: strides must be positive and at most 2^38", name[i]);
+    }
+    jd_status s = check_written(a->out, a->n_tokens, 128, "out");
+    if (s != JD_OK) return s;
+    if (a->n_tokens == 0 || a->n_rows == 0) return JD_OK;
+    if (!a->q.data || !a->k.data || !a->v.data || !a->out.data || !a->cu_seqlens || !a->lambda_q1 || !a->lambda_k1 ||
+        !a->lambda_q2 || !a->lambda_k2)
+        return fail(JD_ERR_INVALID_ARG, "a tensor is NULL");
+    for (const jd_heads *t : {&a->q, &a->k, &a->v, &a->out})
+        if (!heads_aligned(*t, elem, 16)) return fail(JD_ERR_INVALID_ARG, "alignment: pointers and strides of 16 bytes required");
+    for (const jd_heads *t : in)
+        if (t->data == a->out.data) return fail(JD_ERR_INVALID_ARG, "out is an input");
+    DiffOp op{};
+    op.cu = a->cu_seqlens;
+    op.n_rows = a->n_rows;
+    op.n_tokens = a->n_tokens;
+    op.window = a->window < 0 ? -1 : (a->window < a->n_tokens ? a->window : a->n_tokens);
+    op.heads = heads;
+    op.kv_heads = kv;
+    op.qk_dtype = a->qk_dtype;
+    op.v_dtype = a->v_dtype;
+    op.q = a->q.data, op.q_token = a->q.token_stride, op.q_head = a->q.head_stride;
+    op.k = a->k.data, op.k_token = a->k.token_stride, op.k_head = a->k.head_stride;
+    op.v = a->v.data, op.v_token = a->v.token_stride, op.v_head = a->v.head_stride;
+    op.out = a->out.data, op.out_token = a->out.token_stride, op.out_head = a->out.head_stride;
+    op.lq1 = a->lambda_q1, op.lk1 = a->lambda_k1, op.lq2 = a->lambda_q2, op.lk2 = a->lambda_k2;
+    op.gain = a->norm_gain;
+    op.lambda_init = a->lambda_init;
+    op.eps = a->norm_eps;
+    op.scale = a->scale != 0.f ? a->scale : 0.125f;
+    op.status = a->status;
+    OpDevice dev;
+    s = dev.enter({op.q, op.k, op.v, op.out, op.cu, op.lq1, op.lk1, op.lq2, op.lk2, op.gain, op.status});
+    if (s != JD_OK) return s;
+    DiffMaps maps;
+    if (!f32 && (s = make_diff_maps(op, &maps)) != JD_OK) return s;
+    cudaError_t e = diff_attention_prepare(dev.device);
+    if (e == cudaSuccess) e = launch_diff_attention(op, &maps, num_sms(), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(JD_ERR_CUDA, "differential attention: %s", cudaGetErrorString(e));
+    return JD_OK;
+}

@@ -515,6 +515,44 @@ typedef struct {
 /* Normalise every query and key head, then rotate it, in one pass over memory. */
 jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm, void *stream);
 
+/* Differential attention inside each packed row: two softmax maps per head over
+ * one set of values, the second subtracted with a learned weight.
+ *     O_x    = softmax(scale Q_x K_x^T) V                    x = 0, 1
+ *     lambda = exp(lambda_q1 . lambda_k1) - exp(lambda_q2 . lambda_k2) + lambda_init
+ *     D      = O_0 - lambda O_1
+ *     out    = (1 - lambda_init) norm_gain D / sqrt(mean D^2 + norm_eps)
+ * or out = D without norm_gain.  Query and key heads are 64 wide and go in
+ * pairs: head h has queries 2h and 2h + 1, and with kv head g = h / (heads /
+ * kv_heads) keys 2g and 2g + 1 and the 128 wide values g.  Key j is seen by
+ * query i of the same row if window < 0 or |i - j| <= window; a row sees no
+ * other row, whatever the other holds.  Rows may be empty; nothing is written
+ * for tokens past cu_seqlens[n_rows].
+ *   Types: q and k JD_BF16 or JD_F16 with v JD_BF16 or JD_F16, on the tensor
+ *   cores with FP32 sums; or all JD_F32 (FP32 arithmetic).  out has q's type.
+ *   The probabilities enter the second product as FP16 or BF16, as v is; as a
+ *   pair of those (16 bits of mantissa or more) where one alone would show
+ *   beside the rounding of out.
+ *   Pointers and strides lie on 16-byte multiples; input strides are positive.
+ *   out must not overlap an input.
+ * `status` (device, may be NULL) collects the bits of jd_check_status: a
+ * bounded wait that expired (1); the caller clears it. */
+typedef struct {
+    int32_t qk_dtype, v_dtype;
+    int32_t n_tokens, n_rows;  /* >= 0; no tokens or rows: nothing is done */
+    int32_t kv_heads;          /* out.n_heads (heads) is a multiple of it */
+    int32_t window;
+    const int32_t *cu_seqlens; /* device [n_rows + 1], ascending from 0 */
+    jd_heads q, k, v, out;     /* n_heads: 2 heads, 2 kv_heads, kv_heads, heads */
+    const float *lambda_q1, *lambda_k1, *lambda_q2, *lambda_k2; /* device [64] */
+    const float *norm_gain;    /* device [128], or NULL */
+    float lambda_init;
+    float norm_eps;            /* >= 0 */
+    float scale;               /* of the scores, >= 0; 0: 1 / sqrt(64) */
+    uint32_t *status;
+} jd_diff_attention_args;
+
+jd_status jd_diff_attention(const jd_diff_attention_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,3 +46,34 @@ def row_positions(cu, T):
     for a, b in zip(cu[:-1], cu[1:]):
         pos[a:b] = np.arange(b - a)
     return pos
+
+
+def diff_lambda(lq1, lk1, lq2, lk2, lambda_init):
+    return math.exp(float(lq1 @ lk1)) - math.exp(float(lq2 @ lk2)) + lambda_init
+
+
+def diff_attention(q, k, v, cu, lam, lambda_init, gain, eps, window, scale=0.125):
+    """q [T, 2H, 64], k [T, 2G, 64], v [T, G, 128] -> (out [T, H, 128], (D, rms, sums)): the output, the difference
+    before the norm, its root mean square and, per element, sum p0 |v| + |lambda| sum p1 |v| (what errors of the
+    probabilities are multiplied by).  Zero past the last row."""
+    T, H, G = q.shape[0], q.shape[1] // 2, v.shape[1]
+    D, A = np.zeros((T, H, 128)), np.zeros((T, H, 128))
+    for a, b in zip(cu[:-1], cu[1:]):
+        if b <= a:
+            continue
+        i = np.arange(b - a)
+        hidden = np.abs(i[:, None] - i[None, :]) > window if window >= 0 else None
+        for h in range(H):
+            g = h // (H // G)
+            for x, f in ((0, 1.0), (1, -lam)):
+                s = (q[a:b, 2 * h + x] @ k[a:b, 2 * g + x].T) * scale
+                if hidden is not None:
+                    s = np.where(hidden, -np.inf, s)
+                e = np.exp(s - s.max(-1, keepdims=True))
+                p = e / e.sum(-1, keepdims=True)
+                D[a:b, h] += f * (p @ v[a:b, g])
+                A[a:b, h] += abs(f) * (p @ np.abs(v[a:b, g]))
+    if gain is None:
+        return D, (D, None, A)
+    rms = np.sqrt((D * D).mean(-1, keepdims=True) + eps)
+    return (1 - lambda_init) * gain * D / rms, (D, rms, A)

@@ -124,3 +124,75 @@ def test_argument_records_have_the_headers_layout(tmp_path):
                    check=True)
     got = [int(x) for x in re.findall(r"\d+", subprocess.run([str(exe)], capture_output=True, text=True).stdout)]
     assert got == want
+    # the bytes that the binding packs are those structures
+    assert jl._ROTARY_ARGS.size == C.sizeof(jl.jd_rotary_args) and jl._HEAD_NORM.size == C.sizeof(jl.jd_head_norm)
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(5, 7, 16)
+    y, cu, pos = torch.zeros(5, 3, 16), torch.zeros(3, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    rc = jl.rotary_config(8, 3.0, "interleaved", "yarn", 2.0, 77, 30.0, 2.0)
+    data, d = jl._rotary_args(x, y, x.clone(), y.clone(), rc, cu, pos)
+    a = jl.jd_rotary_args.from_buffer_copy(data)
+    assert d == 16 and bytes(a.rotary) == bytes(rc)
+    assert (a.dtype, a.head_dim, a.n_tokens, a.n_rows, a.positions, a.cu_seqlens) == (
+        jl.JD_F32, 16, 5, 2, pos.data_ptr(), cu.data_ptr())
+    assert (a.q.data, a.q.token_stride, a.q.head_stride, a.q.n_heads) == (x.data_ptr(), 112, 16, 7)
+    assert (a.k.data, a.k.token_stride, a.k.n_heads, a.k_out.n_heads) == (y.data_ptr(), 48, 3, 3)
+
+
+def _diff(**kw):
+    h = [_heads(6, base=0x100000), _heads(6, base=0x200000), _heads(3, 128, base=0x300000),
+         _heads(3, 128, base=0x400000)]
+    a = jl.jd_diff_attention_args(jl.JD_BF16, jl.JD_F16, 100, 2, 3, -1, 0x900000, *h, 0x910000, 0x910100, 0x910200,
+                                  0x910300, 0x910400, 0.5, 1e-5, 0.0, None)
+    for name, v in kw.items():
+        obj = a
+        *path, last = name.split("__")
+        for p in path:
+            obj = getattr(obj, p)
+        setattr(obj, last, v)
+    return a
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(qk_dtype=3), "dtype"), (dict(qk_dtype=-1), "dtype"), (dict(v_dtype=0), "v_dtype"),
+    (dict(qk_dtype=0), "v_dtype"), (dict(n_tokens=-1), "negative"), (dict(n_rows=-2), "negative"),
+    (dict(kv_heads=0), "heads"), (dict(kv_heads=2), "heads"), (dict(out__n_heads=0), "heads"),
+    (dict(q__n_heads=5), "heads"), (dict(k__n_heads=3), "heads"), (dict(v__n_heads=6), "heads"),
+    (dict(n_tokens=(1 << 30) + 1), "too many"), (dict(n_rows=1 << 30), "too many"),
+    (dict(lambda_init=float("nan")), "lambda_init"), (dict(norm_eps=-1.0), "norm_eps"),
+    (dict(scale=float("inf")), "scale"), (dict(scale=-0.125), "scale"), (dict(q__token_stride=0), "strides"), (dict(k__head_stride=0), "strides"),
+    (dict(v__token_stride=-8), "strides"), (dict(q__head_stride=1 << 39), "strides"),
+    (dict(out__token_stride=0), "overlap"), (dict(out__head_stride=64), "overlap"),
+    (dict(q__data=None), "NULL"), (dict(cu_seqlens=None), "NULL"), (dict(lambda_k2=None), "NULL"),
+    (dict(q__data=0x100008), "alignment"), (dict(k__token_stride=388), "alignment"),
+    (dict(v__head_stride=132), "alignment"), (dict(out__data=0x400002), "alignment"),
+    (dict(out__data=0x300000), "input"),
+])
+def test_diff_attention_refuses(L, change, word):
+    a = _diff(**change)
+    assert L.jd_diff_attention(C.byref(a), None) == jl.JD_ERR_INVALID_ARG
+    assert word in L.jd_last_error().decode()
+
+
+def test_diff_attention_nothing_to_do_and_null(L):
+    assert L.jd_diff_attention(None, None) == jl.JD_ERR_INVALID_ARG
+    for kw in (dict(n_tokens=0), dict(n_rows=0)):
+        a = _diff(cu_seqlens=None, q__data=None, **kw)
+        assert L.jd_diff_attention(C.byref(a), None) == jl.JD_OK
+
+
+def test_diff_attention_binding_refuses(L):
+    torch = pytest.importorskip("torch")
+    q, k, v, o = torch.zeros(4, 6, 64), torch.zeros(4, 6, 64), torch.zeros(4, 3, 128), torch.zeros(4, 3, 128)
+    cu, lam = torch.zeros(2, dtype=torch.int32), [torch.zeros(64)] * 4
+    for args in ((q, k, v[:3], o), (q, k.half(), v, o), (q, k, v, o.half()), (q[:, :, :32], k, v, o),
+                 (q, k, v[:, :, :64], o), (q[0], k, v, o)):
+        with pytest.raises(jl.JDError):
+            jl.jd_diff_attention(*args, cu, *lam, 0.5)
+    for kw in (dict(norm_gain=torch.ones(64)), dict(status=torch.zeros(1))):
+        with pytest.raises(jl.JDError):
+            jl.jd_diff_attention(q, k, v, o, cu, *lam, 0.5, **kw)
+    with pytest.raises(jl.JDError):
+        jl.jd_diff_attention(q, k, v, o, cu.long(), *lam, 0.5)
+    # the bytes packed are the structure
+    assert jl._DIFF_ARGS.size == C.sizeof(jl.jd_diff_attention_args)
