@@ -5,21 +5,22 @@
 // queries of one row and head; its two maps run side by side, as two query tiles of an ordinary
 // attention would, over the same 128-wide V tiles:
 //
-//   warp 0          TMA producer of the item's Q_0, Q_1 (two buffers) and of K_0, K_1 tiles (a ring of
-//                   16 KB units, freed when their S product completes)
-//   warp 2          TMA producer of V tiles (128 keys x 128, a ring of 32 KB stages)
-//   warp 3          zeroes the rows of an item's last V tile that lie past its keys: their
+//   warp 0          TMA producer: the item's Q_0, Q_1 (two buffers), K_0 and K_1 tiles of 64 keys (a ring
+//                   of 8 KB units, freed when their S product completes), V tiles (64 keys x 128, a
+//                   ring of 16 KB stages)
+//   warp 1, warp 3  lane 0 issues the tcgen05.mma of map 0 and of map 1 (warp 1 holds the TMEM):
+//                     S_x = Q_x K_x^T  (M 128, N 64, K 64)
+//                     O_x += P_x V     (M 128, N 128, K 64; P from TMEM, V read MN-major)
+//   warp 2          zeroes the rows of an item's last V tile that lie past its keys: their
 //                   probabilities are 0, but 0 times what another row holds there may be NaN
-//   warp 1          TMEM; lane 0 issues tcgen05.mma:
-//                     S_x = Q_x K_x^T  (M 128, N 128, K 64)
-//                     O_x += P_x V     (M 128, N 128, K 128; P from TMEM, V read MN-major)
 //   warps 4..7      softmax of map 0, warps 8..11 of map 1: one query row a thread
 //
-// TMEM is full: S_0, S_1 in columns 0..255, O_0, O_1 in 256..511.  P_x overwrites S_x (the thread
-// that stores a row's P has read all of its S), so S_x of the next tile waits for this tile's
-// P_x V; meanwhile the other map's group has the special-function unit.  At an item's end both
-// groups hold the same queries: group x reads columns 64 x .. 64 x + 63 of O_0 and O_1, forms D,
-// and the two halves of a row's sum of squares meet in shared memory.
+// TMEM is full: O_0 and O_1 take 256 columns, and each map has two S tiles of 64 columns in turn, so
+// that its next scores are there while it works on these; P_x overwrites its S tile (the thread that
+// stores a row's P has read all of its S).  One S tile of 128 keys a map, whose next product must
+// wait for P V, ran at 3.08 ms on 16 rows of 8192 with three heads against TIME_LONG here.  At an item's
+// end both groups hold the same queries: group x reads columns 64 x .. 64 x + 63 of O_0 and O_1, forms
+// D, and the two halves of a row's sum of squares meet in shared memory.
 //
 // Bound: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
 // exponentials a clock and SM, 0.094 and 0.125 clocks.
@@ -44,23 +45,27 @@ namespace jd {
 
 namespace {
 
-constexpr int TQ = 128, TK = 128, VD = 128;
+constexpr int TQ = 128, TK = 64, VD = 128;
 constexpr int Q_BYTES = TQ * 128;            // one map's queries: 128 rows x 64 elements of 16 bits
 constexpr int K_BYTES = TK * 128;            // one map's keys
 constexpr int V_HALF = TK * 128;             // 64 columns of a V tile
 constexpr int V_BYTES = 2 * V_HALF;
-constexpr int NK = 4, NV = 2;                // ring depths
+constexpr int NK = 8, NV = 4;                // ring depths
 constexpr int OFF_Q = 0;                     // [item buffer][map]
 constexpr int OFF_K = OFF_Q + 4 * Q_BYTES;
 constexpr int OFF_V = OFF_K + NK * K_BYTES;
 constexpr int OFF_BAR = OFF_V + NV * V_BYTES;
-constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 2 + 1;
+constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 4 + 2 + 1;
 constexpr int OFF_F = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;
 // floats: gain[128], l[2][128], sums of squares[2][128], lambda; then the TMEM slot and a status word
 constexpr int DIFF_SMEM = OFF_F + (128 + 256 + 256 + 4) * 4 + 16 + 1024;
 static_assert(DIFF_SMEM <= 227 * 1024, "differential attention shared memory");
 constexpr uint32_t T_S = 0, T_O = 256;
 constexpr float kLazy = 8.0f;                // log2 headroom before a running max is moved: P <= 2^8
+#ifndef DP
+#define DP 0
+#endif
+constexpr int POLY_OF_8 = DP;
 constexpr int THREADS = 12 * 32;
 // As in the global attention: the compiled count (checked on the host), what warp group 0 keeps and
 // what each softmax group takes.
@@ -93,6 +98,40 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// 2^x for a pair on the FMA and integer pipes.  x = j + f, j = round(x): adding 1.5 * 2^23 leaves j in
+// the low mantissa bits; 2^f on [-1/2, 1/2] is the polynomial of least maximum relative error (Remez
+// exchange): degree 4 off by 2.6e-6, degree 5 by 7.5e-8; j is added to the exponent.  Below -126 the
+// sum of exponents turns negative, which is held at 0; NaN stays NaN or becomes infinite.
+template <int DEGREE>
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+    x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
+    const float2 t = add_f32x2(x, make_float2(12582912.f, 12582912.f));
+    const float2 j = add_f32x2(t, make_float2(-12582912.f, -12582912.f));
+    const float2 f = fma_f32x2(j, make_float2(-1.f, -1.f), x);
+    auto both = [](float c) { return make_float2(c, c); };
+    float2 q;
+    if (DEGREE == 4) {
+        q = fma_f32x2(f, both(0.009570102207362652f), both(0.05591785907745361f));
+        q = fma_f32x2(q, f, both(0.240247443318367f));
+        q = fma_f32x2(q, f, both(0.6931217908859253f));
+        q = fma_f32x2(q, f, both(0.9999992847442627f));
+    } else {
+        q = fma_f32x2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
+        q = fma_f32x2(q, f, both(0.05550713092088699f));
+        q = fma_f32x2(q, f, both(0.24022120237350464f));
+        q = fma_f32x2(q, f, both(0.6931469440460205f));
+        q = fma_f32x2(q, f, both(1.0000001192092896f));
+    }
+    return make_float2(__int_as_float(max(__float_as_int(q.x) + (__float_as_int(t.x) << 23), 0)),
+                       __int_as_float(max(__float_as_int(q.y) + (__float_as_int(t.y) << 23), 0)));
+}
+
 __device__ __forceinline__ void tma_load_heads(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int head, int token) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -101,25 +140,50 @@ __device__ __forceinline__ void tma_load_heads(void *dst, const CUtensorMap *map
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], kind::f16: A is 128 x 16 in TMEM (lane = row, two elements a column)
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// Matrix descriptors, 128-byte swizzle, eight rows 1024 bytes apart (stride).  Q and K: K-major.  V:
+// MN-major, the next 64 elements V_HALF further on (leading).  The upper words are the same; adding
+// to the lower word moves the start, in units of 16 bytes.
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading) {
+    return ((saddr & 0x3FFFFu) >> 4) | (leading << 16);
 }
 
-// MN-major tile with 128-byte swizzle: rows of 64 elements, eight keys 1024 bytes apart (stride), the
-// next 64 elements V_HALF further on (leading).
-__device__ __forceinline__ uint64_t sdesc_v(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(V_HALF >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// S = Q K^T over 64 elements: four steps of 16 (32 bytes of a row each), issued back to back.
+__device__ __forceinline__ void mma_s(uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred on, off;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+        "setp.eq.u32 on, 0, 0;\n\tsetp.ne.u32 off, 0, 0;\n\t"
+        "mov.b64 a0, {%1, %4};\n\tmov.b64 b0, {%2, %4};\n\t"
+        "add.u64 a1, a0, 2;\n\tadd.u64 b1, b0, 2;\n\tadd.u64 a2, a0, 4;\n\tadd.u64 b2, b0, 4;\n\t"
+        "add.u64 a3, a0, 6;\n\tadd.u64 b3, b0, 6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, off;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, on;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, on;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, on;\n\t}" ::"r"(d_tmem),
+        "r"(q_lo), "r"(k_lo), "r"(idesc), "n"(DESC_HI)
+        : "memory");
+}
+// O (+)= P V over 64 keys: four steps of 16 (8 columns of P, 16 rows of V).
+__device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred on, acc;\n\t.reg .b64 b0, b1, b2, b3;\n\t.reg .b32 p1, p2, p3;\n\t"
+        "setp.eq.u32 on, 0, 0;\n\tsetp.ne.u32 acc, %4, 0;\n\t"
+        "mov.b64 b0, {%2, %5};\n\tadd.u64 b1, b0, 128;\n\tadd.u64 b2, b0, 256;\n\tadd.u64 b3, b0, 384;\n\t"
+        "add.u32 p1, %1, 8;\n\tadd.u32 p2, %1, 16;\n\tadd.u32 p3, %1, 24;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %3, acc;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [p1], b1, %3, on;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [p2], b2, %3, on;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [p3], b3, %3, on;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "r"(v_lo), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+        : "memory");
+}
+// One such step (the last keys of a row).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred acc;\n\t.reg .b64 b0;\n\tsetp.ne.u32 acc, %4, 0;\n\tmov.b64 b0, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %3, acc;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "r"(v_lo), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+        : "memory");
 }
 
 struct Item {
@@ -160,6 +224,29 @@ __device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
     return t;
 }
 
+// A walk over the key tiles of this CTA's items (t.on false: past the last).
+struct Walk {
+    Item t;
+    int w, j = 0;
+    uint32_t c = 0, it = 0;
+    __device__ Walk(const DiffOp &p, int n_items, int lane) : w(blockIdx.x) { find(p, n_items, lane); }
+    __device__ void find(const DiffOp &p, int n_items, int lane) {
+        for (t.on = false; w < n_items; w += gridDim.x) {
+            t = find_item(p, w, lane);
+            if (t.on) return;
+        }
+        t.on = false;
+    }
+    __device__ void next(const DiffOp &p, int n_items, int lane) {
+        ++c;
+        if (++j < t.nt) return;
+        j = 0;
+        ++it;
+        w += gridDim.x;
+        find(p, n_items, lane);
+    }
+};
+
 template <bool V16>  // V16: FP16 values, else BF16
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
     return V16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -179,8 +266,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
     uint64_t *qfull = bars, *qfree = qfull + 2, *kfull = qfree + 2, *kfree = kfull + NK, *vfull = kfree + NK,
-             *vfree = vfull + NV, *vtail = vfree + NV, *sfull = vtail + NV, *pready = sfull + 2, *pvdone = pready + 2,
-             *ofree = pvdone + 2;
+             *vfree = vfull + NV, *vtail = vfree + NV, *sfull = vtail + NV, *pready = sfull + 4, *pvdone = pready + 4,
+             *odone = pvdone + 4, *ofree = odone + 2;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
     float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128, *squares = sums + 256,
           *lambda = squares + 256;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lambda + 4);
@@ -194,12 +281,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&vfull[i], 1);
-            mbar_init(&vfree[i], 1);
+            mbar_init(&vfree[i], 2);
             mbar_init(&vtail[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 1);
-            mbar_init(&qfree[i], 1);
+            mbar_init(&qfree[i], 2);
+            mbar_init(&odone[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pready[i], 4);
             mbar_init(&pvdone[i], 1);
@@ -230,58 +320,47 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp < 4) {  // warp group 0: producers, MMA issue, the tail of V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW));
         if (warp == 0) {
-            uint32_t U = 0, it = 0;
-            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-                const Item t = find_item(p, w, lane);
-                if (!t.on) continue;
-                if (lane == 0) {
-                    const int kh = 2 * (t.h / (p.heads / p.kv_heads));
-                    const uint32_t buf = it & 1;
-                    if (it >= 2) mbar_wait(&qfree[buf], ((it - 2) >> 1) & 1, status);
-                    mbar_arrive_expect_tx(&qfull[buf], 2 * Q_BYTES);
-                    for (int x = 0; x < 2; ++x)
-                        tma_load_heads(smem + OFF_Q + (buf * 2 + x) * Q_BYTES, &tm_q, &qfull[buf], 0, 2 * t.h + x, t.q0);
-                    for (int j = 0; j < t.nt; ++j)
-                        for (int x = 0; x < 2; ++x, ++U) {
-                            const uint32_t s = U % NK;
-                            if (U >= NK) mbar_wait(&kfree[s], ((U - NK) / NK) & 1, status);
-                            mbar_arrive_expect_tx(&kfull[s], K_BYTES);
-                            tma_load_heads(smem + OFF_K + s * K_BYTES, &tm_k, &kfull[s], 0, kh + x, t.k0 + j * TK);
-                        }
-                }
-                ++it;
-                __syncwarp();
-            }
-        } else if (warp == 2) {
-            uint32_t J = 0;
+            uint32_t c = 0, it = 0;  // tiles, items
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
                 const Item t = find_item(p, w, lane);
                 if (!t.on) continue;
                 if (lane == 0) {
                     const int vh = t.h / (p.heads / p.kv_heads);
-                    for (int j = 0; j < t.nt; ++j, ++J) {
-                        const uint32_t s = J % NV;
-                        if (J >= NV) mbar_wait(&vfree[s], ((J - NV) / NV) & 1, status);
-                        // a tile that warp 3 has to finish lands on a barrier of its own
+                    const uint32_t buf = it & 1;
+                    if (it >= 2) mbar_wait(&qfree[buf], ((it - 2) >> 1) & 1, status);
+                    mbar_arrive_expect_tx(&qfull[buf], 2 * Q_BYTES);
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_heads(smem + OFF_Q + (buf * 2 + x) * Q_BYTES, &tm_q, &qfull[buf], 0, 2 * t.h + x, t.q0);
+                    for (int j = 0; j < t.nt; ++j, ++c) {
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t u = 2 * c + x, s = u % NK;
+                            if (u >= NK) mbar_wait(&kfree[s], ((u - NK) / NK) & 1, status);
+                            mbar_arrive_expect_tx(&kfull[s], K_BYTES);
+                            tma_load_heads(smem + OFF_K + s * K_BYTES, &tm_k, &kfull[s], 0, 2 * vh + x, t.k0 + j * TK);
+                        }
+                        const uint32_t s = c % NV;
+                        if (c >= NV) mbar_wait(&vfree[s], ((c - NV) / NV) & 1, status);
+                        // a tile that warp 2 has to finish lands on a barrier of its own
                         uint64_t *bar = j == t.nt - 1 && (t.in_last() & 15) ? &vtail[s] : &vfull[s];
                         mbar_arrive_expect_tx(bar, V_BYTES);
                         for (int x = 0; x < 2; ++x)
-                            tma_load_heads(smem + OFF_V + s * V_BYTES + x * V_HALF, &tm_v, bar, 64 * x, vh,
-                                           t.k0 + j * TK);
+                            tma_load_heads(smem + OFF_V + s * V_BYTES + x * V_HALF, &tm_v, bar, 64 * x, vh, t.k0 + j * TK);
                     }
                 }
+                ++it;
                 __syncwarp();
             }
-        } else if (warp == 3) {
-            uint32_t J = 0, tails[NV] = {};
+        } else if (warp == 2) {
+            uint32_t c = 0, tails[NV] = {};
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
                 const Item t = find_item(p, w, lane);
                 if (!t.on) continue;
-                J += t.nt;
+                c += t.nt;
                 const int valid = t.in_last();
                 if ((valid & 15) == 0) continue;  // the MMAs stop at the last whole step of 16 keys
-                const uint32_t s = (J - 1) % NV;
+                const uint32_t s = (c - 1) % NV;
                 mbar_wait(&vtail[s], tails[s]++ & 1, status);
+                __syncwarp();
                 const int pieces = (((valid + 15) & ~15) - valid) * 8;  // 16 bytes each, in both halves
                 for (int i = lane; i < 2 * pieces; i += 32) {
                     uint8_t *half = smem + OFF_V + s * V_BYTES + (i >= pieces ? V_HALF : 0);
@@ -293,60 +372,56 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&vfull[s]);
             }
         } else {
-            const uint32_t qk16 = p.qk_dtype == JD_F16;
-            const uint32_t idesc_s = qk16 ? idesc_f16_f32(TK) : idesc_bf16_f32(TK);
-            const uint32_t idesc_pv = (V16 ? idesc_f16_f32(VD) : idesc_bf16_f32(VD)) | (1u << 16);  // V is MN-major
-            uint32_t U = 0, J = 0, it = 0;
-            uint32_t n_pv[2] = {0, 0};
-            for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-                const Item t = find_item(p, w, lane);
-                if (!t.on) continue;
+            const int x = warp >> 1;  // warp 1: map 0, warp 3: map 1
+            const uint32_t idesc_s = p.qk_dtype == JD_F16 ? idesc_f16_f32(TK) : idesc_bf16_f32(TK);
+            constexpr uint32_t idesc_pv = (V16 ? idesc_f16_f32(VD) : idesc_bf16_f32(VD)) | (1u << 16);  // V is MN-major
+            const uint32_t q_lo = desc_lo(smem_u32(smem + OFF_Q) + x * Q_BYTES, 1), k_lo = desc_lo(smem_u32(smem + OFF_K), 1),
+                           v_lo = desc_lo(smem_u32(smem + OFF_V), V_HALF >> 4);
+            // S products run up to two tiles ahead of the PV products, across items: two walks over the same
+            // tiles.  c counts tiles, it items.
+            Walk at(p, n_items, lane), pv(p, n_items, lane);
+            auto issue_s = [&]() {
+                if (!at.t.on) return;
                 if (lane == 0) {
-                    const uint32_t buf = it & 1;
-                    mbar_wait(&qfull[buf], (it >> 1) & 1, status);
-                    // S_x of tile j: K_x is unit U + 2 j + x; the last P_x must have been used
-                    auto issue_s = [&](int j, int x) {
-                        const uint32_t u = U + 2 * j + x, s = u % NK;
-                        mbar_wait(&kfull[s], (u / NK) & 1, status);
-                        if (n_pv[x]) mbar_wait(&pvdone[x], (n_pv[x] - 1) & 1, status);
-                        tc_fence_after();
-                        const uint32_t q = smem_u32(smem + OFF_Q + (buf * 2 + x) * Q_BYTES);
-                        const uint32_t k = smem_u32(smem + OFF_K + s * K_BYTES);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_bf16(tmem + T_S + TK * x, sdesc_sw128(q + kk * 32), sdesc_sw128(k + kk * 32), idesc_s,
-                                        kk != 0);
-                        tc_commit(&sfull[x]);
-                        tc_commit(&kfree[s]);
-                        if (x == 1 && j == t.nt - 1) tc_commit(&qfree[buf]);
-                    };
-                    issue_s(0, 0);
-                    issue_s(0, 1);
-                    const int valid = t.in_last();
-                    for (int j = 0; j < t.nt; ++j, ++J) {
-                        const uint32_t s = J % NV;
-                        const bool last = j == t.nt - 1;
-                        mbar_wait(&vfull[s], (J / NV) & 1, status);
-                        const int steps = last ? (valid + 15) >> 4 : TK / 16;
-                        const uint32_t v = smem_u32(smem + OFF_V + s * V_BYTES);
-                        for (int x = 0; x < 2; ++x) {
-                            mbar_wait(&pready[x], n_pv[x] & 1, status);
-                            if (j == 0 && x == 0 && it > 0) mbar_wait(ofree, (it - 1) & 1, status);
-                            tc_fence_after();
-                            for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
-                                for (int ks = 0; ks < steps; ++ks)
-                                    mma_ts(tmem + T_O + VD * x, tmem + T_S + TK * x + 64 * part + 8 * ks,
-                                           sdesc_v(v + ks * 16 * 128), idesc_pv, j != 0 || ks != 0 || part != 0);
-                            tc_commit(&pvdone[x]);
-                            ++n_pv[x];
-                            if (x == 1) tc_commit(&vfree[s]);
-                            if (!last) issue_s(j + 1, x);
+                    const uint32_t buf = at.it & 1, b = 2 * x + (at.c & 1), u = 2 * at.c + x, s = u % NK;
+                    if (at.j == 0) mbar_wait(&qfull[buf], (at.it >> 1) & 1, status);
+                    mbar_wait(&kfull[s], (u / NK) & 1, status);
+                    if (at.c >= 2) mbar_wait(&pvdone[b], ((at.c - 2) >> 1) & 1, status);  // its last P has been used
+                    tc_fence_after();
+                    mma_s(tmem + T_S + TK * b, q_lo + buf * (2 * Q_BYTES >> 4), k_lo + s * (K_BYTES >> 4), idesc_s);
+                    tc_commit(&sfull[b]);
+                    tc_commit(&kfree[s]);
+                    if (at.j == at.t.nt - 1) tc_commit(&qfree[buf]);
+                }
+                at.next(p, n_items, lane);
+            };
+            issue_s();
+            issue_s();
+            while (pv.t.on) {
+                if (lane == 0) {
+                    const uint32_t b = 2 * x + (pv.c & 1), s = pv.c % NV;
+                    const bool last = pv.j == pv.t.nt - 1;
+                    mbar_wait(&vfull[s], (pv.c / NV) & 1, status);
+                    mbar_wait(&pready[b], (pv.c >> 1) & 1, status);
+                    if (pv.j == 0 && pv.it > 0) mbar_wait(ofree, (pv.it - 1) & 1, status);
+                    tc_fence_after();
+                    const uint32_t o = tmem + T_O + VD * x, pt = tmem + T_S + TK * b, v = v_lo + s * (V_BYTES >> 4);
+                    const int steps = last ? (pv.t.in_last() + 15) >> 4 : TK / 16;
+                    if (steps == TK / 16) {
+                        mma_pv(o, pt, v, idesc_pv, pv.j != 0);
+                        if (SPLIT) mma_pv(o, pt + 32, v, idesc_pv, 1);
+                    } else {
+                        for (int ks = 0; ks < steps; ++ks) {
+                            mma_ts(o, pt + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, pv.j != 0 || ks != 0);
+                            if (SPLIT) mma_ts(o, pt + 32 + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, 1);
                         }
                     }
-                    U += 2 * t.nt;
+                    tc_commit(&pvdone[b]);
+                    tc_commit(&vfree[s]);
+                    if (last) tc_commit(&odone[x]);
                 }
-                ++it;
-                __syncwarp();
+                issue_s();
+                pv.next(p, n_items, lane);
             }
         }
     } else {
@@ -354,30 +429,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int x = (warp - 4) >> 2;         // this group's map
         const int r = (warp & 3) * 32 + lane;  // query row inside the tile = TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = tl + T_S + TK * x, to = tl + T_O;
+        const uint32_t to = tl + T_O;
         const float sl2 = p.scale * 1.4426950408889634f;
         const float lam = *lambda;
-        uint32_t c = 0;  // tiles of this map so far
+        uint32_t c = 0, it = 0;  // tiles of this map and items so far
         for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
             const Item t = find_item(p, w, lane);
             if (!t.on) continue;
             const int qi = t.q0 + r;
             const bool dead = t.q0 + (warp & 3) * 32 >= t.ce;  // no row of this warp: it only keeps the order
-            // keys this row sees: [lo, hi)
-            const int lo = p.window < 0 ? t.cs : max(t.cs, qi - p.window);
-            const int hi = p.window < 0 ? t.ce : min(t.ce, qi + p.window + 1);
+            // keys this row sees, from the tile's first on: [a, b)
+            int a = (p.window < 0 ? t.cs : max(t.cs, qi - p.window)) - t.k0;
+            int b = (p.window < 0 ? t.ce : min(t.ce, qi + p.window + 1)) - t.k0;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < t.nt; ++j, ++c) {
-                mbar_wait(&sfull[x], c & 1, status);
+            for (int j = 0; j < t.nt; ++j, ++c, a -= TK, b -= TK) {
+                const uint32_t sb = 2 * x + (c & 1), ts = tl + T_S + TK * sb;
+                mbar_wait(&sfull[sb], (c >> 1) & 1, status);
                 __syncwarp();
                 if (!dead) {
                     tc_fence_after();
-                    uint32_t sv[128];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tmem_ld32(ts + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * q]));
+                    uint32_t sv[TK];
+                    tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                    tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                     tmem_ld_wait();
-                    const int a = lo - (t.k0 + j * TK), b = hi - (t.k0 + j * TK);
                     if (__any_sync(0xffffffffu, a > 0 || b < TK)) {
 #pragma unroll
                         for (int e = 0; e < TK; ++e)
@@ -395,11 +469,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
                     // Rows move their maximum one by one, but TMEM is read and written by whole warps (the
                     // instructions are aligned): all rows of the warp go along, most with a factor of 1.
-                    // S_x being there, every earlier PV_x has landed.
                     const bool grows = mx > m + kLazy, scaled = grows && m != -INFINITY;
                     if (__any_sync(0xffffffffu, scaled)) {
                         const float alpha = scaled ? exp2_fast(m - mx) : 1.0f;
                         l *= alpha;
+                        mbar_wait(&pvdone[2 * x + ((c - 1) & 1)], ((c - 1) >> 1) & 1, status);  // O_x is at rest
+                        __syncwarp();
+                        tc_fence_after();
 #pragma unroll 1
                         for (int hc = 0; hc < VD; hc += 32) {
                             uint32_t o[32];
@@ -414,36 +490,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     const float mm = m == -INFINITY ? 0.f : m;  // nothing seen yet: every P is 0
                     float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+                    uint32_t pk[32], pl[SPLIT ? 32 : 1];
 #pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
-                        uint32_t pk[32], pl[SPLIT ? 32 : 1];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float2 xv = fma_f32x2(
-                                make_float2(__uint_as_float(sv[64 * hk + e]), __uint_as_float(sv[64 * hk + e + 1])),
-                                make_float2(sl2, sl2), make_float2(-mm, -mm));
-                            const float p0 = exp2_fast(xv.x), p1 = exp2_fast(xv.y);
-                            ls[(e >> 1) & 3] = add_f32x2(ls[(e >> 1) & 3], make_float2(p0, p1));
-                            pk[e >> 1] = pack_p<V16>(p0, p1);
-                            if (SPLIT) {
-                                const float2 h = unpack_p<V16>(pk[e >> 1]);
-                                pl[e >> 1] = pack_p<V16>(p0 - h.x, p1 - h.y);
-                            }
+                    for (int e = 0; e < TK; e += 2) {
+                        const float2 xv =
+                            fma_f32x2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                      make_float2(sl2, sl2), make_float2(-mm, -mm));
+                        const float2 pv = ((e >> 1) & 7) < POLY_OF_8 ? exp2_poly<SPLIT ? 5 : 4>(xv)
+                                                                     : make_float2(exp2_fast(xv.x), exp2_fast(xv.y));
+                        ls[(e >> 1) & 3] = add_f32x2(ls[(e >> 1) & 3], pv);
+                        pk[e >> 1] = pack_p<V16>(pv.x, pv.y);
+                        if (SPLIT) {
+                            const float2 h = unpack_p<V16>(pk[e >> 1]);
+                            pl[e >> 1] = pack_p<V16>(pv.x - h.x, pv.y - h.y);
                         }
-                        tmem_st32(ts + 32 * hk, pk);
-                        if constexpr (SPLIT) tmem_st32(ts + 64 + 32 * hk, pl);
                     }
+                    tmem_st32(ts, pk);
+                    if constexpr (SPLIT) tmem_st32(ts + 32, pl);
                     l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
                     tmem_st_wait();
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pready[x]);
+                if (lane == 0) mbar_arrive(&pready[sb]);
             }
             // Both maps' sums, then this group's half of the columns of both O
             sums[128 * x + r] = l;
-            mbar_wait(&pvdone[0], (c - 1) & 1, status);
-            mbar_wait(&pvdone[1], (c - 1) & 1, status);
+            mbar_wait(&odone[0], it & 1, status);
+            mbar_wait(&odone[1], it & 1, status);
+            ++it;
             __syncwarp();
             named_bar_sync(BAR_SUMS, 256);
             float d[64], sq = 0.f;
@@ -687,17 +762,17 @@ jd_status make_diff_maps(const DiffOp &op, DiffMaps *maps) {
     struct {
         CUtensorMap *m;
         const void *data;
-        int width, heads, dtype;
+        int width, heads, rows, dtype;
         int64_t token, head;
-    } t[3] = {{&maps->q, op.q, 64, 2 * op.heads, op.qk_dtype, op.q_token, op.q_head},
-              {&maps->k, op.k, 64, 2 * op.kv_heads, op.qk_dtype, op.k_token, op.k_head},
-              {&maps->v, op.v, 128, op.kv_heads, op.v_dtype, op.v_token, op.v_head}};
+    } t[3] = {{&maps->q, op.q, 64, 2 * op.heads, TQ, op.qk_dtype, op.q_token, op.q_head},
+              {&maps->k, op.k, 64, 2 * op.kv_heads, TK, op.qk_dtype, op.k_token, op.k_head},
+              {&maps->v, op.v, 128, op.kv_heads, TK, op.v_dtype, op.v_token, op.v_head}};
     for (auto &a : t) {
         // an axis of one entry is never stepped along: any stride does
         const cuuint64_t dims[3] = {(cuuint64_t)a.width, (cuuint64_t)a.heads, (cuuint64_t)op.n_tokens};
         const cuuint64_t strides[2] = {2 * (cuuint64_t)(a.heads > 1 ? a.head : a.width),
                                        2 * (cuuint64_t)(op.n_tokens > 1 ? a.token : a.width)};
-        const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)a.rows}, es[3] = {1, 1, 1};
         const CUresult r =
             fn(a.m, a.dtype == JD_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                const_cast<void *>(a.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,

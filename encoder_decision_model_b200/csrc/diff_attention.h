@@ -23,7 +23,8 @@ struct DiffOp {
     unsigned *status;
 };
 
-// Maps of q, k and v for the tensor-core kernel: (element, head, token), boxes of 64 x 1 x 128.
+// Maps of q, k and v for the tensor-core kernel: (element, head, token), boxes of 64
+// elements of one head and 128 (q) or 64 tokens.
 struct DiffMaps {
     CUtensorMap q, k, v;
 };
