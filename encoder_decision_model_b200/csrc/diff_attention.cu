@@ -186,6 +186,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t p_tmem, uint32_
         : "memory");
 }
 
+// The bounded wait, with its slow half out of the way: the roles run through their loops once a tile,
+// between warps whose unrolled loops fill the instruction cache, so every instruction here counts.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, unsigned *status) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if (it & 255u) continue;
+        if (*reinterpret_cast<volatile unsigned *>(status) & ST_WAIT_TIMEOUT) return;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > 2000000000ull) {
+            atomicOr(status, ST_WAIT_TIMEOUT);
+            return;
+        }
+    }
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 struct Item {
     int h, cs, ce, q0;   // head, row, first query
     int k0, kend, nt;    // keys [k0, kend) in nt tiles
@@ -223,29 +246,6 @@ __device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
     t.nt = (t.kend - t.k0 + TK - 1) / TK;
     return t;
 }
-
-// A walk over the key tiles of this CTA's items (t.on false: past the last).
-struct Walk {
-    Item t;
-    int w, j = 0;
-    uint32_t c = 0, it = 0;
-    __device__ Walk(const DiffOp &p, int n_items, int lane) : w(blockIdx.x) { find(p, n_items, lane); }
-    __device__ void find(const DiffOp &p, int n_items, int lane) {
-        for (t.on = false; w < n_items; w += gridDim.x) {
-            t = find_item(p, w, lane);
-            if (t.on) return;
-        }
-        t.on = false;
-    }
-    __device__ void next(const DiffOp &p, int n_items, int lane) {
-        ++c;
-        if (++j < t.nt) return;
-        j = 0;
-        ++it;
-        w += gridDim.x;
-        find(p, n_items, lane);
-    }
-};
 
 template <bool V16>  // V16: FP16 values, else BF16
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
@@ -377,51 +377,73 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t idesc_pv = (V16 ? idesc_f16_f32(VD) : idesc_bf16_f32(VD)) | (1u << 16);  // V is MN-major
             const uint32_t q_lo = desc_lo(smem_u32(smem + OFF_Q) + x * Q_BYTES, 1), k_lo = desc_lo(smem_u32(smem + OFF_K), 1),
                            v_lo = desc_lo(smem_u32(smem + OFF_V), V_HALF >> 4);
-            // S products run up to two tiles ahead of the PV products, across items: two walks over the same
-            // tiles.  c counts tiles, it items.
-            Walk at(p, n_items, lane), pv(p, n_items, lane);
-            auto issue_s = [&]() {
-                if (!at.t.on) return;
-                if (lane == 0) {
-                    const uint32_t buf = at.it & 1, b = 2 * x + (at.c & 1), u = 2 * at.c + x, s = u % NK;
-                    if (at.j == 0) mbar_wait(&qfull[buf], (at.it >> 1) & 1, status);
-                    mbar_wait(&kfull[s], (u / NK) & 1, status);
-                    if (at.c >= 2) mbar_wait(&pvdone[b], ((at.c - 2) >> 1) & 1, status);  // its last P has been used
-                    tc_fence_after();
-                    mma_s(tmem + T_S + TK * b, q_lo + buf * (2 * Q_BYTES >> 4), k_lo + s * (K_BYTES >> 4), idesc_s);
-                    tc_commit(&sfull[b]);
-                    tc_commit(&kfree[s]);
-                    if (at.j == at.t.nt - 1) tc_commit(&qfree[buf]);
-                }
-                at.next(p, n_items, lane);
+            const uint32_t b_sfull = smem_u32(sfull + 2 * x), b_pready = smem_u32(pready + 2 * x),
+                           b_pvdone = smem_u32(pvdone + 2 * x), b_kfull = smem_u32(kfull), b_kfree = smem_u32(kfree),
+                           b_vfull = smem_u32(vfull), b_vfree = smem_u32(vfree);
+            uint32_t sc = 0, c = 0, it = 0;  // S and PV products issued, items
+            // the next S product, of an item whose queries are in buffer buf
+            auto issue_s = [&](uint32_t buf, bool last) {
+                const uint32_t b = sc & 1, u = 2 * sc + x, s = u % NK;
+                wait(b_kfull + 8 * s, (u / NK) & 1, status);
+                if (sc >= 2) wait(b_pvdone + 8 * b, ((sc - 2) >> 1) & 1, status);  // its last P has been used
+                tc_fence_after();
+                mma_s(tmem + T_S + 2 * TK * x + TK * b, q_lo + buf * (2 * Q_BYTES >> 4), k_lo + s * (K_BYTES >> 4), idesc_s);
+                commit(b_sfull + 8 * b);
+                commit(b_kfree + 8 * s);
+                if (last) commit(smem_u32(&qfree[buf]));
+                ++sc;
             };
-            issue_s();
-            issue_s();
-            while (pv.t.on) {
+            // S products run up to two tiles ahead of the PV products, into the next item if it has come to that
+            int w = blockIdx.x, ahead = 0;  // ahead: S products of the current item issued so far
+            auto find_on = [&]() {
+                Item t;
+                for (t.on = false; w < n_items && !t.on; w += gridDim.x) t = find_item(p, w, lane);
+                return t;
+            };
+            Item now = find_on();
+            while (now.on) {
+                const Item next = find_on();
                 if (lane == 0) {
-                    const uint32_t b = 2 * x + (pv.c & 1), s = pv.c % NV;
-                    const bool last = pv.j == pv.t.nt - 1;
-                    mbar_wait(&vfull[s], (pv.c / NV) & 1, status);
-                    mbar_wait(&pready[b], (pv.c >> 1) & 1, status);
-                    if (pv.j == 0 && pv.it > 0) mbar_wait(ofree, (pv.it - 1) & 1, status);
-                    tc_fence_after();
-                    const uint32_t o = tmem + T_O + VD * x, pt = tmem + T_S + TK * b, v = v_lo + s * (V_BYTES >> 4);
-                    const int steps = last ? (pv.t.in_last() + 15) >> 4 : TK / 16;
-                    if (steps == TK / 16) {
-                        mma_pv(o, pt, v, idesc_pv, pv.j != 0);
-                        if (SPLIT) mma_pv(o, pt + 32, v, idesc_pv, 1);
-                    } else {
-                        for (int ks = 0; ks < steps; ++ks) {
-                            mma_ts(o, pt + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, pv.j != 0 || ks != 0);
-                            if (SPLIT) mma_ts(o, pt + 32 + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, 1);
+                    const uint32_t buf = it & 1;
+                    if (ahead == 0) wait(smem_u32(&qfull[buf]), (it >> 1) & 1, status);
+                    while (ahead < min(2, now.nt)) ++ahead, issue_s(buf, ahead == now.nt);
+                    int nahead = 0;
+                    for (int j = 0; j < now.nt; ++j, ++c) {
+                        const uint32_t b = c & 1, s = c % NV;
+                        wait(b_vfull + 8 * s, (c / NV) & 1, status);
+                        wait(b_pready + 8 * b, (c >> 1) & 1, status);
+                        if (j == 0 && it > 0) wait(smem_u32(ofree), (it - 1) & 1, status);
+                        tc_fence_after();
+                        const uint32_t o = tmem + T_O + VD * x, pt = tmem + T_S + 2 * TK * x + TK * b,
+                                       v = v_lo + s * (V_BYTES >> 4);
+                        const bool last = j == now.nt - 1;
+                        const int steps = last ? (now.in_last() + 15) >> 4 : TK / 16;
+                        if (steps == TK / 16) {
+                            mma_pv(o, pt, v, idesc_pv, j);
+                            if (SPLIT) mma_pv(o, pt + 32, v, idesc_pv, 1);
+                        } else {
+                            for (int ks = 0; ks < steps; ++ks) {
+                                mma_ts(o, pt + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, j | ks);
+                                if (SPLIT) mma_ts(o, pt + 32 + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, 1);
+                            }
+                        }
+                        commit(b_pvdone + 8 * b);
+                        commit(b_vfree + 8 * s);
+                        if (last) commit(smem_u32(&odone[x]));
+                        if (ahead < now.nt) {
+                            ++ahead;
+                            issue_s(buf, ahead == now.nt);
+                        } else if (next.on && nahead < min(2, next.nt)) {
+                            if (nahead == 0) wait(smem_u32(&qfull[buf ^ 1]), ((it + 1) >> 1) & 1, status);
+                            ++nahead;
+                            issue_s(buf ^ 1, nahead == next.nt);
                         }
                     }
-                    tc_commit(&pvdone[b]);
-                    tc_commit(&vfree[s]);
-                    if (last) tc_commit(&odone[x]);
+                    ahead = nahead;
+                    ++it;
                 }
-                issue_s();
-                pv.next(p, n_items, lane);
+                __syncwarp();
+                now = next;
             }
         }
     } else {
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int x = (warp - 4) >> 2;         // this group's map
         const int r = (warp & 3) * 32 + lane;  // query row inside the tile = TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t to = tl + T_O;
+        const uint32_t to = tl + T_O, b_sfull = smem_u32(sfull + 2 * x), b_pready = smem_u32(pready + 2 * x);
         const float sl2 = p.scale * 1.4426950408889634f;
         const float lam = *lambda;
         uint32_t c = 0, it = 0;  // tiles of this map and items so far
@@ -443,8 +465,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             int b = (p.window < 0 ? t.ce : min(t.ce, qi + p.window + 1)) - t.k0;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < t.nt; ++j, ++c, a -= TK, b -= TK) {
-                const uint32_t sb = 2 * x + (c & 1), ts = tl + T_S + TK * sb;
-                mbar_wait(&sfull[sb], (c >> 1) & 1, status);
+                const uint32_t ts = tl + T_S + 2 * TK * x + TK * (c & 1);
+                wait(b_sfull + 8 * (c & 1), (c >> 1) & 1, status);
                 __syncwarp();
                 if (!dead) {
                     tc_fence_after();
@@ -512,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pready[sb]);
+                if (lane == 0) arrive(b_pready + 8 * (c & 1));
             }
             // Both maps' sums, then this group's half of the columns of both O
             sums[128 * x + r] = l;
