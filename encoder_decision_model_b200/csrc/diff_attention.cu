@@ -202,6 +202,12 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, unsigned *st
         }
     }
 }
+// One lane of a converged warp; the compiler knows that only one thread goes on.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Item now = find_on();
             while (now.on) {
                 const Item next = find_on();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t buf = it & 1;
                     if (ahead == 0) wait(smem_u32(&qfull[buf]), (it >> 1) & 1, status);
                     while (ahead < min(2, now.nt)) ++ahead, issue_s(buf, ahead == now.nt);
