@@ -253,6 +253,13 @@ __device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
     return t;
 }
 
+// The next item that is not empty, from w on; w moves past it.
+__device__ __forceinline__ Item find_on(const DiffOp &p, int &w, int n_items, int lane) {
+    Item t;
+    for (t.on = false; w < n_items && !t.on; w += gridDim.x) t = find_item(p, w, lane);
+    return t;
+}
+
 template <bool V16>  // V16: FP16 values, else BF16
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
     return V16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -401,14 +408,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             // S products run up to two tiles ahead of the PV products, into the next item if it has come to that
             int w = blockIdx.x, ahead = 0;  // ahead: S products of the current item issued so far
-            auto find_on = [&]() {
-                Item t;
-                for (t.on = false; w < n_items && !t.on; w += gridDim.x) t = find_item(p, w, lane);
-                return t;
-            };
-            Item now = find_on();
+            Item now = find_on(p, w, n_items, lane);
             while (now.on) {
-                const Item next = find_on();
+                const Item next = find_on(p, w, n_items, lane);
                 if (elect_one()) {
                     const uint32_t buf = it & 1;
                     if (ahead == 0) wait(smem_u32(&qfull[buf]), (it >> 1) & 1, status);
@@ -461,9 +463,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float sl2 = p.scale * 1.4426950408889634f;
         const float lam = *lambda;
         uint32_t c = 0, it = 0;  // tiles of this map and items so far
-        for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-            const Item t = find_item(p, w, lane);
-            if (!t.on) continue;
+        int w = blockIdx.x;
+        Item next = find_on(p, w, n_items, lane);
+        while (next.on) {
+            const Item t = next;
             const int qi = t.q0 + r;
             const bool dead = t.q0 + (warp & 3) * 32 >= t.ce;  // no row of this warp: it only keeps the order
             // keys this row sees, from the tile's first on: [a, b)
@@ -544,6 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // Both maps' sums, then this group's half of the columns of both O
             sums[128 * x + r] = l;
+            next = find_on(p, w, n_items, lane);  // while the last products finish
             mbar_wait(&odone[0], it & 1, status);
             mbar_wait(&odone[1], it & 1, status);
             ++it;
@@ -577,16 +581,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (qi * p.out_token + t.h * p.out_head + 64 * x);
                 const bool out16 = p.qk_dtype == JD_F16;
 #pragma unroll
-                for (int e = 0; e < 64; e += 8) {
-                    const float4 g0 = *reinterpret_cast<const float4 *>(&gain[64 * x + e]),
-                                 g1 = *reinterpret_cast<const float4 *>(&gain[64 * x + e + 4]);
-                    const float y[8] = {d[e] * f * g0.x,     d[e + 1] * f * g0.y, d[e + 2] * f * g0.z, d[e + 3] * f * g0.w,
-                                        d[e + 4] * f * g1.x, d[e + 5] * f * g1.y, d[e + 6] * f * g1.z, d[e + 7] * f * g1.w};
-                    uint32_t u[4];
+                for (int e = 0; e < 64; e += 16) {
+                    uint32_t u[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        u[i] = out16 ? pack_f16x2(y[2 * i], y[2 * i + 1]) : pack_bf16x2(y[2 * i], y[2 * i + 1]);
-                    *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float4 g = *reinterpret_cast<const float4 *>(&gain[64 * x + e + 2 * i]);
+                        const float v[4] = {d[e + 2 * i] * f * g.x, d[e + 2 * i + 1] * f * g.y, d[e + 2 * i + 2] * f * g.z,
+                                            d[e + 2 * i + 3] * f * g.w};
+                        u[i] = out16 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]);
+                        u[i + 1] = out16 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]);
+                    }
+                    if (p.out32) {  // a row a thread: 32-byte stores fill whole sectors
+                        st_global_v8(dst + 2 * e, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4 *>(dst + 2 * e + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                    }
                 }
             }
         }
@@ -902,6 +912,7 @@ extern "C" jd_status jd_diff_attention(const jd_diff_attention_args *a, void *st
     op.k = a->k.data, op.k_token = a->k.token_stride, op.k_head = a->k.head_stride;
     op.v = a->v.data, op.v_token = a->v.token_stride, op.v_head = a->v.head_stride;
     op.out = a->out.data, op.out_token = a->out.token_stride, op.out_head = a->out.head_stride;
+    op.out32 = heads_aligned(a->out, elem, 32);
     op.lq1 = a->lambda_q1, op.lk1 = a->lambda_k1, op.lq2 = a->lambda_q2, op.lk2 = a->lambda_k2;
     op.gain = a->norm_gain;
     op.lambda_init = a->lambda_init;

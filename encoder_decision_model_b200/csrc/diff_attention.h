@@ -18,6 +18,7 @@ struct DiffOp {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head;
     void *out;
     int64_t out_token, out_head;
+    bool out32;                    // out and its strides on 32-byte multiples
     const float *lq1, *lk1, *lq2, *lk2, *gain;
     float lambda_init, eps, scale;
     unsigned *status;
