@@ -477,7 +477,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t ts = tl + T_S + 2 * TK * x + TK * (c & 1);
                 wait(b_sfull + 8 * (c & 1), (c >> 1) & 1, status);
                 __syncwarp();
-                if (!dead) {
+                if (!dead && !__any_sync(0xffffffffu, a < TK && b > 0)) {
+                    // none of this warp's rows sees any of these keys (the ends of a window)
+                    tc_fence_after();
+                    uint32_t zero[32] = {};
+                    tmem_st32(ts, zero);
+                    if constexpr (SPLIT) tmem_st32(ts + 32, zero);
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else if (!dead) {
                     tc_fence_after();
                     uint32_t sv[TK];
                     tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
