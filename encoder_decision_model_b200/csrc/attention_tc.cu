@@ -430,26 +430,27 @@ __global__ void __launch_bounds__(ATC_THREADS, 1)
                     for (int a = 0; a < 4; ++a)
                         m4[a] = fmax3(m4[a], __uint_as_float(sv[e + 2 * a]), __uint_as_float(sv[e + 2 * a + 1]));
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-                if (mx > m + kLazy) {
-                    if (m != -INFINITY) {
-                        const float alpha = ex2_approx(m - mx);
-                        l *= alpha;
-                        mbar_wait(&pvdone[x], (c - 1) & 1, status);  // every PV product on O_x has landed
-                        __syncwarp();
-                        tc_fence_after();
+                // Rows move their maximum one by one, but TMEM is read and written by whole warps (the
+                // instructions are aligned): all rows of the warp go along, most with a factor of 1.
+                const bool grows = mx > m + kLazy, scaled = grows && m != -INFINITY;
+                if (__any_sync(0xffffffffu, scaled)) {
+                    const float alpha = scaled ? ex2_approx(m - mx) : 1.0f;
+                    l *= alpha;
+                    mbar_wait(&pvdone[x], (c - 1) & 1, status);  // every PV product on O_x has landed
+                    __syncwarp();
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int hc = 0; hc < 64; hc += 32) {  // 32 columns at a time: S stays in registers
-                            uint32_t o[32];
-                            tmem_ld32(tl + T_O + 64 * x + hc, o);
-                            tmem_ld_wait();
+                    for (int hc = 0; hc < 64; hc += 32) {  // 32 columns at a time: S stays in registers
+                        uint32_t o[32];
+                        tmem_ld32(tl + T_O + 64 * x + hc, o);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tl + T_O + 64 * x + hc, o);
-                        }
-                        tmem_st_wait();
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(tl + T_O + 64 * x + hc, o);
                     }
-                    m = mx;
+                    tmem_st_wait();
                 }
+                if (grows) m = mx;
                 if (pp) {
                     if (x == 0) {
                         if (j != 0 || g0_wait_first) named_bar_sync(BAR_G1_DONE, 256);
