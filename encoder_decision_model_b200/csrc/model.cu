@@ -8,6 +8,11 @@
 //   Wi GEMM + GEGLU      y = GELU(u) * g
 //   Wo2 GEMM + residual  x += y Wo2^T; xn = LN_attn(l+1)(x)
 //     (last layer: h = LN_final(x) + type row, xn = LN1 of head layer 0)
+// A weights file may give encoder layers norms of their query and key heads and differential
+// attention, and the rotation another layout, width or scaling; then per such layer
+//   QKV GEMM             xn -> qkv                 (unrotated, where the GEMM cannot rotate as asked)
+//   norms and rotation   qkv -> qkv                (one pass, in place)
+//   diff attention       qkv -> o                  (in place of attention: 3 heads of two maps)
 // Head layer 0 (all tokens) and head layer 1 (keys / values for all tokens,
 // everything else only at the markers), scorer, read-outs.
 //
@@ -32,6 +37,8 @@
 #include "host_common.h"
 #include "kernels.h"
 #include "batch_pad.h"
+#include "diff_attention.h"
+#include "rotary.h"
 #include "route_kernels.h"
 
 using namespace jd;
@@ -193,6 +200,17 @@ struct jd_model {
     float *sc_g = nullptr, *sc_b = nullptr, *sc_w1t = nullptr, *sc_b1 = nullptr, *sc_w2 = nullptr, *sc_b2 = nullptr;
     float *lin_w = nullptr, *lin_b = nullptr;
     float4 *rope_g = nullptr, *rope_l = nullptr;  // [16][MAX_POS] (cos, sin) of pairs 2k, 2k + 1
+    // optional tensors of the encoder layers (null: the layer has none)
+    float *qn[NL] = {}, *kn[NL] = {};             // gains of the query and key head norms [64]
+    float *lam[NL] = {}, *dn[NL] = {};            // differential attention: q1, k1, q2, k2 [4][64]; norm gain [128]
+    // rotation of the global and the local layers (0, 1): `fused` into the QKV GEMM through rope_g / rope_l
+    struct Rotation {
+        bool fused = true;
+        int dims = DH;
+        bool interleaved = false;
+        float amplitude = 1.f;
+        std::array<double, DH / 2> turns{};
+    } rot[2];
 
     // workspace
     float *x = nullptr;
@@ -211,6 +229,7 @@ struct jd_model {
     CUtensorMap to_qkv{}, to_y_enc{}, to_y_head{}, to_qm{}, to_ym{};
     CUtensorMap tm_x32{};  // FP32 residual stream, box 32 x 128
     CUtensorMap tm_qkv128{};  // q|k|v, box 64 x 128 (tensor-core attention)
+    DiffMaps tm_diff{};       // q, k and v heads of the differential attention
 
     // internal outputs (jd_forward, host entry points) and device batch staging
     float *i_logits = nullptr, *i_probs = nullptr, *i_score = nullptr, *i_noul = nullptr, *i_maxp = nullptr;
@@ -387,6 +406,75 @@ jd_status make_rope_table(jd_model *m, double theta, float4 **dst) {
     return JD_OK;
 }
 
+// The rotation that a layer kind's record in enc.rotary asks for: layout, dims, theta, scaling, factor,
+// original length, beta_fast, beta_slow.  What the QKV GEMM rotates itself (half layout, whole head, any
+// scaling) gets a table, in the layout of make_rope_table.
+jd_status set_rotation(jd_model *m, const float *rec, jd_model::Rotation &r, float4 **table) {
+    for (int i = 0; i < 8; ++i)
+        if (!std::isfinite(rec[i])) return fail(JD_ERR_IO, "tensor enc.rotary: value %d is not finite", i);
+    auto whole = [](float v) { return v == std::floor(v) && std::fabs(v) <= 16777216.f ? (int)v : -1; };
+    const jd_rotary_config c{whole(rec[0]), whole(rec[1]), rec[2], whole(rec[3]), whole(rec[5]), rec[4], rec[6], rec[7]};
+    double turns[ROTARY_MAX_PAIRS] = {};
+    const jd_status s = rotary_turns(c, DH, turns, &r.amplitude);
+    if (s != JD_OK) return fail(JD_ERR_IO, "tensor enc.rotary: %s", std::string(jd_last_error()).c_str());
+    std::copy(turns, turns + DH / 2, r.turns.begin());
+    r.dims = c.dims;
+    r.interleaved = c.layout == JD_ROTARY_INTERLEAVED;
+    r.fused = !r.interleaved && c.dims == DH;
+    if (!r.fused) return JD_OK;
+    std::vector<float4> h((size_t)16 * MAX_POS);
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int k = 0; k < 16; ++k)
+        for (int p = 0; p < MAX_POS; ++p) {
+            const double a0 = two_pi * (p * turns[2 * k]), a1 = two_pi * (p * turns[2 * k + 1]), f = r.amplitude;
+            h[(size_t)k * MAX_POS + p] = make_float4((float)(f * std::cos(a0)), (float)(f * std::sin(a0)),
+                                                     (float)(f * std::cos(a1)), (float)(f * std::sin(a1)));
+        }
+    TRY(m->dalloc(table, h.size()));
+    CK(cudaMemcpy(*table, h.data(), h.size() * sizeof(float4), cudaMemcpyHostToDevice));
+    return JD_OK;
+}
+
+// The encoder layers' optional tensors: head norms, differential attention, the rotation.
+jd_status load_variants(jd_model *m, WeightFile &wf) {
+    auto has = [&](const std::string &n) { return wf.idx.count(n) != 0; };
+    for (int l = 0; l < NL; ++l) {
+        const std::string p = "enc." + std::to_string(l) + ".";
+        if (has(p + "q_norm.g") || has(p + "k_norm.g")) {
+            TRY(upload_f32(m, wf, p + "q_norm.g", {DH}, &m->qn[l]));
+            TRY(upload_f32(m, wf, p + "k_norm.g", {DH}, &m->kn[l]));
+        }
+        const char *names[5] = {"lambda_q1", "lambda_k1", "lambda_q2", "lambda_k2", "diff_norm.g"};
+        bool any = false;
+        for (const char *n : names) any = any || has(p + n);
+        if (!any) continue;
+        std::vector<float> all, one;
+        for (int i = 0; i < 4; ++i) {
+            TRY(read_tensor(wf, p + names[i], {DH}, one));
+            all.insert(all.end(), one.begin(), one.end());
+        }
+        TRY(m->dalloc(&m->lam[l], all.size()));
+        CK(cudaMemcpy(m->lam[l], all.data(), all.size() * 4, cudaMemcpyHostToDevice));
+        TRY(upload_f32(m, wf, p + names[4], {2 * DH}, &m->dn[l]));
+    }
+    const double base[2] = {160000.0, 10000.0};  // global, local
+    float4 **table[2] = {&m->rope_g, &m->rope_l};
+    std::vector<float> rec;
+    if (has("enc.rotary")) TRY(read_tensor(wf, "enc.rotary", {2, 8}, rec));
+    for (int i = 0; i < 2; ++i) {
+        if (!rec.empty()) {
+            TRY(set_rotation(m, rec.data() + 8 * i, m->rot[i], table[i]));
+            continue;
+        }
+        const jd_rotary_config plain{JD_ROTARY_HALF, DH, base[i], JD_SCALING_NONE, 0, 1.0, 0.0, 0.0};
+        double turns[ROTARY_MAX_PAIRS];
+        TRY(rotary_turns(plain, DH, turns, &m->rot[i].amplitude));
+        std::copy(turns, turns + DH / 2, m->rot[i].turns.begin());
+        TRY(make_rope_table(m, base[i], table[i]));
+    }
+    return JD_OK;
+}
+
 // Copy the weight pointers and their tensor maps of m into v (no device memory is allocated).
 void share_weights(jd_model &v, const jd_model *m) {
     v.E = m->E; v.emb_g = m->emb_g; v.fin_g = m->fin_g; v.type_tab = m->type_tab;
@@ -402,7 +490,37 @@ void share_weights(jd_model &v, const jd_model *m) {
     }
     v.sc_g = m->sc_g; v.sc_b = m->sc_b; v.sc_w1t = m->sc_w1t; v.sc_b1 = m->sc_b1; v.sc_w2 = m->sc_w2;
     v.sc_b2 = m->sc_b2; v.lin_w = m->lin_w; v.lin_b = m->lin_b; v.rope_g = m->rope_g; v.rope_l = m->rope_l;
-    for (int l = 0; l < NL; ++l) v.inv8[l] = m->inv8[l];
+    for (int l = 0; l < NL; ++l) {
+        v.inv8[l] = m->inv8[l];
+        v.qn[l] = m->qn[l]; v.kn[l] = m->kn[l]; v.lam[l] = m->lam[l]; v.dn[l] = m->dn[l];
+    }
+    v.rot[0] = m->rot[0]; v.rot[1] = m->rot[1];
+}
+
+// Differential attention over a q|k|v workspace of n_tokens tokens: the six query heads as three pairs,
+// the same of the keys, three value heads of 128.  Values are FP16 beside BF16 queries and keys (the QKV
+// GEMM writes them so), or all is FP32.
+DiffOp diff_op(void *qkv, void *o, int n_tokens, bool fp32) {
+    const size_t es = fp32 ? 4 : 2;
+    DiffOp d{};
+    d.n_tokens = n_tokens;
+    d.window = -1;
+    d.heads = d.kv_heads = NH / 2;
+    d.qk_dtype = fp32 ? JD_F32 : JD_BF16;
+    d.v_dtype = fp32 ? JD_F32 : JD_F16;
+    d.q = qkv;
+    d.k = static_cast<uint8_t *>(qkv) + D * es;
+    d.v = static_cast<uint8_t *>(qkv) + 2 * D * es;
+    d.q_token = d.k_token = d.v_token = QKV;
+    d.q_head = d.k_head = DH;
+    d.v_head = 2 * DH;
+    d.out = o;
+    d.out_token = D;
+    d.out_head = 2 * DH;
+    d.out32 = true;
+    d.eps = EPS;
+    d.scale = 0.125f;
+    return d;
 }
 
 jd_status load_weights(jd_model *m, const char *path) {
@@ -474,9 +592,7 @@ jd_status load_weights(jd_model *m, const char *path) {
     TRY(upload_f32(m, wf, "scorer.linear2.b", {1}, &m->sc_b2));
     TRY(upload_f32(m, wf, "scorer_lin.W", {1, d}, &m->lin_w));
     TRY(upload_f32(m, wf, "scorer_lin.b", {1}, &m->lin_b));
-    TRY(make_rope_table(m, 160000.0, &m->rope_g));
-    TRY(make_rope_table(m, 10000.0, &m->rope_l));
-    return JD_OK;
+    return load_variants(m, wf);
 }
 
 jd_status alloc_host_slot(jd_model *m, jd_model::HostSlot &h) {
@@ -555,7 +671,9 @@ jd_status alloc_workspace(jd_model *m) {
         TRY(make_map(&m->to_y_head, m->y, HFF, T, HFF, 64, 32));
         TRY(make_map(&m->to_qm, m->qm, D, M, D, 64, 32));
         TRY(make_map(&m->to_ym, m->ym, HFF, M, HFF, 64, 32));
+        TRY(make_diff_maps(diff_op(m->qkv, m->o, (int)T, false), &m->tm_diff));
     }
+    CK(diff_attention_prepare(m->device));
     return JD_OK;
 }
 
@@ -644,7 +762,9 @@ jd_status enqueue_forward(jd_model *m, const jd_batch *b, const jd_outputs *out,
         EpiParams e = base_ep(m, T);
         e.out = m->qkv;
         e.ldo = QKV;
-        e.rope = glob ? m->rope_g : m->rope_l;
+        const jd_model::Rotation &rot = m->rot[glob ? 0 : 1];
+        const bool rotate = m->qn[l] || !rot.fused;  // in a pass of its own, behind the GEMM
+        e.rope = rotate ? nullptr : (glob ? m->rope_g : m->rope_l);
         e.pos = m->pos;
         e.rope_cols = 2 * D;
         if (f8) {
@@ -657,8 +777,44 @@ jd_status enqueue_forward(jd_model *m, const jd_batch *b, const jd_outputs *out,
             KL("gemm_qkv_rope", 1, launch_gemm(make_op(EPI_QKV, 384, m->Wqkv[l], &m->tm_xn, m->xn, D, e, &m->to_qkv), f32, st));
         }
 
+        if (rotate) {
+            RotaryOp r{};
+            r.n_tokens = T;
+            r.n_rows = B;
+            r.positions = m->pos;
+            r.dtype = f32 ? JD_F32 : JD_BF16;
+            r.head_dim = DH;
+            r.dims = rot.dims;
+            r.interleaved = rot.interleaved;
+            r.amplitude = rot.amplitude;
+            std::copy(rot.turns.begin(), rot.turns.end(), r.turns);
+            for (int i = 0; i < 2; ++i) {
+                r.src[i] = r.dst[i] = offset<uint8_t>(m->qkv, (size_t)i * D, f32);
+                r.src_token[i] = r.dst_token[i] = QKV;
+                r.src_head[i] = r.dst_head[i] = DH;
+                r.n_heads[i] = NH;
+            }
+            r.in_place = true;
+            r.norm = m->qn[l] != nullptr;
+            r.eps = EPS;
+            r.gain[0] = m->qn[l];
+            r.gain[1] = m->kn[l];
+            rotary_plan(r, true);
+            KL(r.norm ? "qk_norm_rotary" : "rotary", 1, launch_rotary(r, st));
+        }
         aa.window = glob ? -1 : 64;
-        KL(glob ? "attn_global" : "attn_local", 1, launch_attention(aa, f32, st));
+        if (m->lam[l]) {
+            DiffOp d = diff_op(m->qkv, m->o, T, f32);
+            d.cu = b->cu_seqlens;
+            d.n_rows = B;
+            d.window = aa.window;
+            d.lq1 = m->lam[l], d.lk1 = d.lq1 + DH, d.lq2 = d.lk1 + DH, d.lk2 = d.lq2 + DH;
+            d.gain = m->dn[l];
+            d.lambda_init = 0.8f - 0.6f * std::exp(-0.3f * l);
+            d.status = m->status;
+            KL(glob ? "attn_diff_global" : "attn_diff_local", 1, launch_diff_attention(d, &m->tm_diff, num_sms(), st));
+        } else
+            KL(glob ? "attn_global" : "attn_local", 1, launch_attention(aa, f32, st));
 
         e = base_ep(m, T);
         e.out = m->xn;
@@ -1496,6 +1652,7 @@ struct NoAllocSlot {
     CUtensorMap to_qkv{}, to_y_enc{}, to_y_head{}, to_qm{}, to_ym{};
     CUtensorMap tm_x32{};  // FP32 residual stream, box 32 x 128
     CUtensorMap tm_qkv128{};
+    DiffMaps tm_diff{};
 };
 NoAllocSlot g_na_slot[NA_MAX_DEVICES];
 std::mutex g_na_mutex;
@@ -1530,6 +1687,7 @@ jd_status noalloc_setup(int dev) {
     TRY(make_map(&s.to_y_head, s.base + NA_Y, HFF, NA_TOKENS, HFF, 64, 32));
     TRY(make_map(&s.to_qm, s.base + NA_QM, D, NA_MARKERS, D, 64, 32));
     TRY(make_map(&s.to_ym, s.base + NA_YM, HFF, NA_MARKERS, HFF, 64, 32));
+    TRY(make_diff_maps(diff_op(s.base + NA_QKV, s.base + NA_O, NA_TOKENS, false), &s.tm_diff));
     s.ready = true;
     return JD_OK;
 }
@@ -1557,6 +1715,7 @@ void noalloc_view(jd_model &v, const jd_model *m, const NoAllocSlot &s) {
     v.to_qkv = s.to_qkv; v.to_y_enc = s.to_y_enc; v.to_y_head = s.to_y_head; v.to_qm = s.to_qm; v.to_ym = s.to_ym;
     v.tm_x32 = s.tm_x32;
     v.tm_qkv128 = s.tm_qkv128;
+    v.tm_diff = s.tm_diff;
     v.prof = false;
     v.graph_mode = false;
 }

@@ -194,7 +194,18 @@ jd_status jd_rows_encoding_info(const jd_row *rows, int32_t n_rows, const jd_enc
  * capacity on `device` (the architecture of "The decision head" and "Julia-1
  * MLX", "Performance": 22 encoder layers of width 384, a 3 x 384 type table,
  * two head layers, the scorer).  BF16 copies of the projection weights are
- * made here; the embedding table, norms, biases and head stay FP32.  On
+ * made here; the embedding table, norms, biases and head stay FP32.
+ * The file may carry further tensors of the encoder layers l, which every entry
+ * point of the model then runs (the operators at the end of this header):
+ *   enc.<l>.q_norm.g, enc.<l>.k_norm.g [64]  RMS norms (eps 1e-5) of every query
+ *       and key head before the rotation;
+ *   enc.<l>.lambda_q1, lambda_k1, lambda_q2, lambda_k2 [64], diff_norm.g [128]
+ *       differential attention: the six heads as three of two maps, values 128
+ *       wide, lambda_init 0.8 - 0.6 exp(-0.3 l), within the layer's window;
+ *   enc.rotary [2, 8]  the rotation of the global and of the local layers: layout,
+ *       dims, theta, scaling, factor, original_length, beta_fast, beta_slow
+ *       (jd_rotary_config's values as floats).
+ * On
  * success *out is a handle the caller owns and releases with
  * jd_model_destroy (NULL is accepted there); on failure *out is NULL.
  * Errors: JD_ERR_INVALID_ARG (NULL argument, a capacity < 1, unknown

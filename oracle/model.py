@@ -31,6 +31,9 @@ plausible):
   * attention scale 1/sqrt(64); head attention has no positional encoding;
   * head feed-forward activation ReLU (flag "gelu"); scorer "mlp" (flag
     "linear": LayerNorm -> Linear(384 -> 1)).
+A weights file may give encoder layers RMS norms of their query and key heads,
+differential attention and another rotation (the header's jd_model_create); they
+are computed where their tensors are present.
 Arithmetic is float64 end to end; weights are the float32 values of the file.
 Parity: each function is pinned in tests/test_oracle_model.py by closed forms,
 brute force on tiny inputs and invariants, and the whole chain (encoder ->
@@ -111,6 +114,45 @@ def gelu(x):
     return 0.5 * x * (1.0 + erf(x / math.sqrt(2.0)))
 
 
+def rms_norm(x, g, eps=1e-5):
+    """x / sqrt(mean x^2 + eps) * g over the last axis."""
+    return x / np.sqrt((x * x).mean(axis=-1, keepdims=True) + eps) * g
+
+
+def rotation(rec):
+    """(pairing, angle per position of each pair, factor of cos and sin) of an enc.rotary record:
+    layout (0 half, 1 interleaved), dims, theta, scaling (0 none, 1 linear, 2 NTK, 3 YaRN), factor,
+    original length, beta_fast, beta_slow."""
+    layout, r, theta, scaling, f, length, fast, slow = (float(v) for v in rec)
+    r = int(r)
+    if scaling == 2 and r > 2:
+        theta = theta * f ** (r / (r - 2))
+    w, amp = theta ** (-np.arange(0, r, 2, dtype=F) / r), 1.0
+    if scaling == 1:
+        w = w / f
+    if scaling == 3:
+        def pair(turns):
+            return r * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(theta))
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), r - 1)
+        g = np.clip((np.arange(r // 2) - low) / max(high - low, 1e-3), 0, 1)
+        w = (1 - g) * w + g * w / f
+        amp = 0.1 * math.log(f) + 1 if f > 1 else 1.0
+    return int(layout), w, amp
+
+
+def rope_as(x, rec):
+    """Rotary embedding of x [L, H, dh] by an enc.rotary record; elements past dims pass through."""
+    layout, w, amp = rotation(rec)
+    h = len(w)
+    ang = np.arange(x.shape[0], dtype=F)[:, None] * w[None, :]
+    c, s = amp * np.cos(ang)[:, None, :], amp * np.sin(ang)[:, None, :]
+    i, j = (slice(0, h), slice(h, 2 * h)) if layout == 0 else (slice(0, 2 * h, 2), slice(1, 2 * h, 2))
+    y = x.copy()
+    y[..., i] = x[..., i] * c - x[..., j] * s
+    y[..., j] = x[..., j] * c + x[..., i] * s
+    return y
+
+
 def rope(x, theta):
     """Rotary embedding of x [L, H, dh]; pairs (i, i + dh/2), positions 0..L-1."""
     L, _, dh = x.shape
@@ -147,6 +189,34 @@ def attention(q, k, v, window=None):
     return out
 
 
+def diff_attention(q, k, v, W, p, l, window, eps):
+    """Differential attention of one row: heads 2h and 2h + 1 of q and k [L, H, dh] are the two maps of
+    head h, over values of 2 dh; the difference of the maps is normalised head by head."""
+    L, H, dh = q.shape
+    v = v.reshape(L, H // 2, 2 * dh)
+    start = 0.8 - 0.6 * math.exp(-0.3 * l)
+    lam = math.exp(W[p + "lambda_q1"] @ W[p + "lambda_k1"]) - math.exp(W[p + "lambda_q2"] @ W[p + "lambda_k2"]) + start
+    i = np.arange(L)
+    hidden = np.abs(i[:, None] - i[None, :]) > (L if window is None else window)
+    out = np.empty((L, H // 2, 2 * dh))
+    for h in range(H // 2):
+        maps = []
+        for x in (0, 1):
+            s = (q[:, 2 * h + x] @ k[:, 2 * h + x].T) / math.sqrt(dh)
+            maps.append(softmax_rows(np.where(hidden, -np.inf, s)))
+        d = (maps[0] - lam * maps[1]) @ v[:, h]
+        out[:, h] = (1 - start) * rms_norm(d, W[p + "diff_norm.g"], eps)
+    return out
+
+
+def optional(W, name):
+    """A tensor that a weights file may leave out."""
+    try:
+        return W[name]
+    except KeyError:
+        return None
+
+
 @dataclass
 class ModelOptions:
     scorer: str = "mlp"        # "mlp" | "linear"
@@ -171,8 +241,19 @@ def encoder_layer(x, W, l, mo: ModelOptions):
     q, k, v = (qkv[:, i * d:(i + 1) * d].reshape(L, H, dh) for i in range(3))
     is_global = (l % mo.global_every) == 0
     theta = mo.theta_global if is_global else mo.theta_local
-    q, k = rope(q, theta), rope(k, theta)
-    o = attention(q, k, v, window=None if is_global else mo.window)
+    window = None if is_global else mo.window
+    gains = optional(W, p + "q_norm.g")
+    if gains is not None:
+        q, k = rms_norm(q, gains, mo.eps), rms_norm(k, W[p + "k_norm.g"], mo.eps)
+    rotary = optional(W, "enc.rotary")
+    if rotary is None:
+        q, k = rope(q, theta), rope(k, theta)
+    else:
+        q, k = rope_as(q, rotary[0 if is_global else 1]), rope_as(k, rotary[0 if is_global else 1])
+    if optional(W, p + "lambda_q1") is None:
+        o = attention(q, k, v, window=window)
+    else:
+        o = diff_attention(q, k, v, W, p, l, window, mo.eps)
     x = x + o.reshape(L, d) @ W[p + "Wo"].T
     ug = layer_norm(x, W[p + "mlp_norm.g"], eps=mo.eps) @ W[p + "Wi"].T
     f = ug.shape[1] // 2

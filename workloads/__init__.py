@@ -8,6 +8,7 @@ from .gen import (  # noqa: F401
     ARCH,
     Row,
     RouterRequest,
+    variant_tensors,
     weight_specs,
     write_weights,
     weights_path,

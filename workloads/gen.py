@@ -17,6 +17,9 @@ File format (".jdw", little endian):
     zero padding to a multiple of 256 bytes, then the data section:
     every tensor in float32, C order, each starting on a 256-byte boundary.
 
+A file may also carry the encoder layers' optional tensors (variant_tensors):
+head norms, differential attention and the rotation's settings.
+
 Rows: pre-tokenized requests whose ids are uniform in [10, 256000) (ids 0..9
 are reserved for special tokens).  The five workload recipes are stated on
 each function.
@@ -111,13 +114,37 @@ def weights_path(seed: int = 0, std: float = 0.02, tag: str = "") -> Path:
     return path
 
 
-def write_weights(path, seed: int = 0, std: float = 0.02, overrides=None):
+def variant_tensors(seed: int = 0, norms=(), diff=(), rotary=None, gain: float = 1.0):
+    """Optional tensors of the encoder layers, for write_weights(extra=...).
+
+    `norms`: layers whose query and key heads are normalised (gains around `gain`);
+    `diff`: layers with differential attention; `rotary`: two records (global, local)
+    of layout, dims, theta, scaling, factor, original length, beta_fast, beta_slow.
+    """
+    rng = np.random.Generator(np.random.PCG64([seed, 1]))
+    dh, out = ARCH["head_dim"], {}
+    for l in norms:
+        for n in ("q_norm.g", "k_norm.g"):
+            out[f"enc.{l}.{n}"] = gain * (1 + 0.1 * rng.standard_normal(dh))
+    for l in diff:
+        for n in ("lambda_q1", "lambda_k1", "lambda_q2", "lambda_k2"):
+            out[f"enc.{l}.{n}"] = 0.1 * rng.standard_normal(dh)
+        out[f"enc.{l}.diff_norm.g"] = 1 + 0.1 * rng.standard_normal(2 * dh)
+    if rotary is not None:
+        out["enc.rotary"] = np.asarray(rotary, np.float64)
+    return {k: v.astype(np.float32) for k, v in out.items()}
+
+
+def write_weights(path, seed: int = 0, std: float = 0.02, overrides=None, extra=None):
     """Draw every tensor from one PCG64 stream in spec order and write a .jdw file.
 
     `overrides` maps tensor name -> callable(array) -> array applied after the
     draw (used by tests that scale a tensor); it does not change the stream.
+    `extra` maps further tensor names to arrays, written behind the others
+    (the encoder layers' optional tensors: variant_tensors).
     """
-    specs = weight_specs()
+    extra = {k: np.ascontiguousarray(v, np.float32) for k, v in (extra or {}).items()}
+    specs = weight_specs() + [(k, v.shape, "extra") for k, v in extra.items()]
     rng = np.random.Generator(np.random.PCG64(seed))
     header_len = 8 + 4 + REC_SIZE * len(specs)
     data_start = (header_len + ALIGN - 1) // ALIGN * ALIGN
@@ -141,6 +168,8 @@ def write_weights(path, seed: int = 0, std: float = 0.02, overrides=None):
                 arr = rng.standard_normal(n, dtype=np.float32) * np.float32(std)
             elif kind == "ones":
                 arr = np.ones(n, np.float32)
+            elif kind == "extra":
+                arr = extra[name].reshape(-1)
             else:
                 arr = np.zeros(n, np.float32)
             if overrides and name in overrides:
