@@ -14,8 +14,8 @@
 // 32 bits the angle at position 10^5 is off by 4e-3), and sine and cosine of the fraction are FP32.
 //
 // Two kernels: k_rotary as above, where head_dim and the two runs fall on 16-byte vectors, and
-// k_rotary_any for every other width, offset and stride (a head through shared memory, eight
-// elements a lane).
+// k_rotary_any for every other width, offset and stride (a thread holds eight elements and finds
+// their partners where the other threads' are kept).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,8 +29,6 @@
 namespace jd {
 
 namespace {
-
-constexpr int WARPS = 8;
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -109,39 +107,10 @@ __device__ __forceinline__ Vec8<T> pack8(const float *y) {
     }
     return x;
 }
-// Elements that are read once need not stay in the caches.
-template <typename T>
-__device__ __forceinline__ Vec8<T> stream8(const T *p) {
-    Vec8<T> x;
-#pragma unroll
-    for (int i = 0; i < Vec8<T>::N; ++i) x.v[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-    return x;
-}
 template <typename T>
 __device__ __forceinline__ void put8(T *p, const Vec8<T> &x) {
 #pragma unroll
     for (int i = 0; i < Vec8<T>::N; ++i) reinterpret_cast<uint4 *>(p)[i] = x.v[i];
-}
-
-// Eight elements of a head from element e0 on; past head_dim zeros are read and nothing is written.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(float *y, const T *p, int e0, int head_dim) {
-    if (VEC) {
-        unpack8(stream8(p + e0), y);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = e0 + j < head_dim ? to_f(p[e0 + j]) : 0.f;
-    }
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T *p, const float *y, int e0, int head_dim) {
-    if (VEC) {
-        put8(p + e0, pack8<T>(y));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (e0 + j < head_dim) p[e0 + j] = from_f<T>(y[j]);
-    }
 }
 
 // Row of token t: the last r with cu[r] <= t, found by 32 probes at a time; -1 for a token outside
@@ -218,7 +187,14 @@ __device__ __forceinline__ void join_pairs(float *z, const float2 *a, const floa
 
 constexpr int VWARPS = 4;         // warps of a k_rotary CTA
 constexpr int AHEAD = 3;          // heads on their way to each thread
-constexpr int CTAS_PER_SM = 32;   // CTAs of a launch, at most, for each SM
+#ifndef ROT_T
+#define ROT_T 8
+#endif
+#ifndef ROT_R
+#define ROT_R 5
+#endif
+constexpr int CTAS_RESIDENT = ROT_R;  // CTAs that an SM holds at once
+constexpr int CTAS_PER_SM = 32;   // CTAs of a large launch, at most, for each SM
 
 // NORM: 0 none, 1 RMS, 2 layer norm
 template <typename T, bool INTERLEAVED, int NORM>
@@ -426,166 +402,186 @@ __global__ void __launch_bounds__(32 * VWARPS) k_rotary(const __grid_constant__ 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Any head_dim, dims and strides.  A thread holds one run of eight elements; the half layout's partners
+// lie in other threads' runs, wherever half = r/2 puts them, and are read from their place in the ring.
+// VEC: head_dim, pointers and strides allow 16-byte pieces; else elements are loaded one by one.
 template <typename T, bool INTERLEAVED, bool NORM, bool VEC>
-__global__ void __launch_bounds__(32 * WARPS) k_rotary_any(const __grid_constant__ RotaryOp op) {
-    __shared__ float2 cs_all[WARPS][ROTARY_MAX_PAIRS];
-    __shared__ float swap_all[INTERLEAVED ? 1 : WARPS][INTERLEAVED ? 1 : 32 * 8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float2 *cs = cs_all[warp];
-    float *swap = swap_all[INTERLEAVED ? 0 : warp];
-    const int r = op.dims, half = r >> 1;
-
-    double turns[ROTARY_MAX_PAIRS / 32];
-#pragma unroll
-    for (int i = 0; i < ROTARY_MAX_PAIRS / 32; ++i) {
-        const int j = lane + 32 * i;
-        turns[i] = j < half ? op.turns[j] : 0.0;
-    }
-    const int G = op.lanes_per_head;      // lanes of one head: a power of two
-    const int e0 = (lane & (G - 1)) * 8;  // this lane's first element, the same in every head
-    const int heads_at_once = 32 / G, sub = lane / G;
+__global__ void __launch_bounds__(32 * VWARPS) k_rotary_any(const __grid_constant__ RotaryOp op) {
+    constexpr int PIECES = Vec8<T>::N, PER = 16 / sizeof(T);  // elements of a piece
+    __shared__ uint4 ring[AHEAD + 1][PIECES][32 * VWARPS];
+    __shared__ float2 angles[32 * VWARPS * 4];  // cosine, sine; at most four pairs a thread
+    __shared__ double turns[ROTARY_MAX_PAIRS];
+    const int lane = threadIdx.x & 31;
+    const int L = op.lanes_per_head, HS = op.heads_at_once, TPT = L * HS;
+    const int in_token = threadIdx.x & (TPT - 1), unit = in_token & (L - 1), hs = in_token / L;
+    const int r = op.dims, half = r >> 1, e0 = 8 * unit, head_dim = op.head_dim;
     const int n_heads = op.n_heads[0] + op.n_heads[1];
-    const bool live = e0 < op.head_dim;
-    // in place and without a norm the elements past r keep their values where they are
-    const bool skip = !live || (!NORM && op.in_place && e0 >= r);
-    const float inv_n = 1.0f / (float)op.head_dim;
-
-    // a CTA walks consecutive tokens, a warp one at a time, and follows their rows
+    const bool live = e0 < head_dim;
+    // in place and without a norm the runs past r keep their values where they are
+    const bool on = live && (NORM || !op.in_place || e0 < r);
+    const float inv_n = 1.0f / (float)head_dim;
+    float2 *cs = angles + (threadIdx.x / TPT) * (4 * L);
+    for (int j = threadIdx.x; j < half; j += 32 * VWARPS) turns[j] = op.turns[j];
+    __syncthreads();
+    const int at_once = 32 / TPT, step = VWARPS * at_once;
     const int begin = blockIdx.x * op.tokens_per_cta, last = min(op.n_tokens, begin + op.tokens_per_cta);
-    if (begin + warp >= last) return;
+    const int first = begin + (threadIdx.x >> 5) * at_once;
+    if (first >= last) return;
+
+    int next_t = first + lane / TPT, next_h = hs, next_place = 0;  // the next head to ask for
+    auto place_of = [&](const void *base, int64_t token, int64_t head, int t, int h) {
+        return static_cast<const T *>(base) + t * token + h * head + e0;
+    };
+    auto ask = [&]() {
+        if (on && next_t < last && next_h < n_heads) {
+            const int w = next_h < op.n_heads[0] ? 0 : 1;
+            const T *p = place_of(op.src[w], op.src_token[w], op.src_head[w], next_t, next_h - (w ? op.n_heads[0] : 0));
+            if (VEC) {
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    copy_async16(&ring[next_place][i][threadIdx.x], reinterpret_cast<const uint4 *>(p) + i);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    reinterpret_cast<T *>(&ring[next_place][j / PER][threadIdx.x])[j % PER] =
+                        e0 + j < head_dim ? p[j] : from_f<T>(0.f);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next_place = next_place == AHEAD ? 0 : next_place + 1;
+        next_h += HS;
+        if (next_h - hs >= n_heads) {
+            next_h = hs;
+            next_t += step;
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < AHEAD; ++i) ask();
+
     int row = -1, row_start = 0, row_end = op.n_tokens;
     if (!op.positions) {
-        row = row_of(op.cu, op.n_rows, begin + warp, lane);
-        if (row < 0) return;
-        row_start = op.cu[row];
-        row_end = op.cu[row + 1];
+        row = row_of(op.cu, op.n_rows, first, lane);
+        row_start = row < 0 ? 0 : op.cu[row];
+        row_end = row < 0 ? 0 : op.cu[row + 1];  // past every row: nothing to do, and nothing follows
     }
-    for (int t = begin + warp; t < last; t += WARPS) {
-        float x[4][8];
-        auto load = [&](int h0) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int hh = h0 + u * heads_at_once + sub;
-                if (hh < n_heads && !skip) {
-                    const int w = hh < op.n_heads[0] ? 0 : 1;
-                    const int h = w ? hh - op.n_heads[0] : hh;
-                    load8<T, VEC>(x[u], static_cast<const T *>(op.src[w]) + t * op.src_token[w] + h * op.src_head[w], e0,
-                                  op.head_dim);
-                }
-            }
-        };
-        load(0);
-        int pos;
+    int place = 0;
+    for (int t0 = first; t0 < last; t0 += step) {
+        const int t = t0 + lane / TPT;
+        bool work = on && t < last;
+        int pos = 0;
         if (op.positions) {
-            pos = op.positions[t];
+            if (t < last) pos = op.positions[t];
         } else {
-            while (t >= row_end && row + 1 < op.n_rows) {
+            while (row >= 0 && t >= row_end && row + 1 < op.n_rows) {
                 ++row;
                 row_start = row_end;
                 row_end = op.cu[row + 1];
             }
-            if (t >= row_end) return;
+            work = work && t < row_end;
             pos = t - row_start;
         }
-#pragma unroll
-        for (int i = 0; i < ROTARY_MAX_PAIRS / 32; ++i) {
-            if (32 * i < half) {
-                double a = (double)pos * turns[i];
-                a -= rint(a);
-                float s, c;
-                sincospif(2.0f * (float)a, &s, &c);
-                cs[lane + 32 * i] = make_float2(op.amplitude * c, op.amplitude * s);
-            }
+        __syncwarp();  // the last tokens' sines have been read
+        for (int j = in_token; j < half; j += TPT) {
+            double a = (double)pos * turns[j];
+            a -= rint(a);
+            float s, c;
+            sincospif(2.0f * (float)a, &s, &c);
+            cs[j] = make_float2(op.amplitude * c, op.amplitude * s);
         }
         __syncwarp();
-        float c[8], s[8];  // of this lane's elements; s carries the sign of the partner's share
+        float c[8], s[8];  // of this thread's elements; s carries the sign of the partner's share
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = e0 + j;
-            const bool first = INTERLEAVED ? (e & 1) == 0 : e < half;
-            const int pair = INTERLEAVED ? e >> 1 : (first ? e : e - half);
-            const float2 v = e < r ? cs[pair] : make_float2(1.f, 0.f);
+            const bool one = INTERLEAVED ? (e & 1) == 0 : e < half;  // a of its pair, or b
+            const float2 v = e < r ? cs[INTERLEAVED ? e >> 1 : (one ? e : e - half)] : make_float2(1.f, 0.f);
             c[j] = v.x;
-            s[j] = first ? -v.y : v.y;
+            s[j] = one ? -v.y : v.y;
         }
-        __syncwarp();
 
-        for (int h0 = 0; h0 < n_heads; h0 += 4 * heads_at_once) {
-            if (h0) load(h0);
+#pragma unroll 1
+        for (int h = hs; h - hs < n_heads; h += HS) {
+            ask();
+            asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+            if (!INTERLEAVED) __syncwarp();  // the other threads' runs are there too
+            float y[8], q[8];
+            const bool mine = work && h < n_heads;
+            const int w = h < op.n_heads[0] ? 0 : 1;
+            {
+                Vec8<T> x;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (h0 + u * heads_at_once >= n_heads) break;  // the same for the whole warp
-                const int hh = h0 + u * heads_at_once + sub;
-                const bool on = hh < n_heads && !skip;
-                const int w = hh < op.n_heads[0] ? 0 : 1;
-                float y[8];
+                for (int i = 0; i < PIECES; ++i) x.v[i] = ring[place][i][threadIdx.x];
+                unpack8(x, y);
+            }
+            int partner[8];
+            if (!INTERLEAVED) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = on ? x[u][j] : 0.f;
-                if (NORM) {
-                    if (op.layer_norm) {
-                        float m = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-                        for (int o = G >> 1; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-                        m *= inv_n;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[j] = VEC || e0 + j < op.head_dim ? y[j] - m : 0.f;
-                        if (!live) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = 0.f;
-                        }
-                    }
-                    float q = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) q = fmaf(y[j], y[j], q);
-                    for (int o = G >> 1; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-                    const float f = rsqrtf(fmaf(q, inv_n, op.eps));
-                    const float *g = w ? op.gain[1] : op.gain[0];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        y[j] *= f;
-                        if (g && e0 + j < op.head_dim) y[j] *= __ldg(g + e0 + j);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const int e = e0 + j;
+                    partner[j] = e < r ? (e < half ? e + half : e - half) : e;
+                    const int in = partner[j] & 7;
+                    q[j] = to_f(reinterpret_cast<const T *>(&ring[place][in / PER][threadIdx.x - unit + (partner[j] >> 3)])[in % PER]);
                 }
-                float p[8];
-                if (INTERLEAVED) {
+                __syncwarp();  // read: the place may be asked for again
+            }
+            place = place == AHEAD ? 0 : place + 1;
+            if (NORM) {
+                if (!mine) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = y[j ^ 1];
-                } else {
-                    float *mine = swap + sub * G * 8;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) mine[e0 + j] = y[j];
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int e = e0 + j;
-                        p[j] = e < r ? mine[e < half ? e + half : e - half] : 0.f;
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 8; ++j) y[j] = 0.f;
                 }
-                float z[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)  // past r the partner is another element: it must not enter (0 * inf)
-                    z[j] = e0 + j < r ? fmaf(y[j], c[j], p[j] * s[j]) : y[j];
-                if (on) {
-                    const int h = w ? hh - op.n_heads[0] : hh;
-                    store8<T, VEC>(static_cast<T *>(op.dst[w]) + t * op.dst_token[w] + h * op.dst_head[w], z, e0,
-                                   op.head_dim);
+                float m = 0.f;
+                if (op.layer_norm) {
+                    m = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+                    for (int o = L >> 1; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+                    m *= inv_n;
                 }
+                float sq = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = e0 + j < head_dim ? y[j] - m : 0.f;
+                    sq = fmaf(y[j], y[j], sq);
+                }
+                for (int o = L >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                const float f = rsqrtf(fmaf(sq, inv_n, op.eps));
+                const float *g = op.gain[w];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] *= g && e0 + j < head_dim ? f * __ldg(g + e0 + j) : f;
+                    if (!INTERLEAVED) q[j] = (q[j] - m) * (g && partner[j] < head_dim ? f * __ldg(g + partner[j]) : f);
+                }
+            }
+            if (INTERLEAVED) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[j] = y[j ^ 1];
+            }
+            if (!mine) continue;
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // past r nothing else may enter (0 * inf)
+                z[j] = e0 + j < r ? fmaf(y[j], c[j], q[j] * s[j]) : y[j];
+            T *p = const_cast<T *>(place_of(op.dst[w], op.dst_token[w], op.dst_head[w], t, h - (w ? op.n_heads[0] : 0)));
+            if (VEC) {
+                put8(p, pack8<T>(z));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (e0 + j < head_dim) p[j] = from_f<T>(z[j]);
             }
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T, bool INTERLEAVED>
 void launch_typed(const RotaryOp &op, cudaStream_t st) {
+    const dim3 g(op.ctas), b(32 * VWARPS);
     if (op.vec) {
-        const dim3 g(op.ctas), b(32 * VWARPS);
         if (!op.norm) k_rotary<T, INTERLEAVED, 0><<<g, b, 0, st>>>(op);
         else if (!op.layer_norm) k_rotary<T, INTERLEAVED, 1><<<g, b, 0, st>>>(op);
         else k_rotary<T, INTERLEAVED, 2><<<g, b, 0, st>>>(op);
         return;
     }
-    const dim3 b(32 * WARPS);
-    const dim3 g(op.ctas);
     if (op.vec8) {
         if (op.norm) k_rotary_any<T, INTERLEAVED, true, true><<<g, b, 0, st>>>(op);
         else k_rotary_any<T, INTERLEAVED, false, true><<<g, b, 0, st>>>(op);
@@ -614,10 +610,13 @@ void rotary_plan(RotaryOp &op, bool aligned) {
     while (op.heads_at_once < 4 && op.heads_at_once * 2 <= op.n_heads[0] + op.n_heads[1] &&
            op.heads_at_once * 2 * op.lanes_per_head <= 32)
         op.heads_at_once *= 2;
-    // tokens of one step of a CTA; at most 32 CTAs an SM, which even out their ends, walk the rest
-    const int per_step = op.vec ? VWARPS * 32 / (op.lanes_per_head * op.heads_at_once) : WARPS;
-    const int steps = (op.n_tokens + per_step - 1) / per_step;
-    op.tokens_per_cta = (steps + 148 * CTAS_PER_SM - 1) / (148 * CTAS_PER_SM) * per_step;
+    // Tokens of one step of a CTA, and how many steps a CTA takes.  Small calls: as many CTAs as are resident
+    // at once, so that their start (a row search, the frequencies) is paid once.  From ROT_T steps each
+    // on more CTAs than that even out the SMs' ends.
+    const int per_step = VWARPS * 32 / (op.lanes_per_head * op.heads_at_once);
+    const int steps = (op.n_tokens + per_step - 1) / per_step, resident = 148 * CTAS_RESIDENT;
+    const int ctas = steps < ROT_T * resident ? resident : 148 * CTAS_PER_SM;
+    op.tokens_per_cta = (steps + ctas - 1) / ctas * per_step;
     op.ctas = (op.n_tokens + op.tokens_per_cta - 1) / op.tokens_per_cta;
 }
 
