@@ -618,17 +618,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ FP32
 
-constexpr int FQ = 64, FK = 64, FP = 68;  // queries and keys of a tile; padded row of a transposed tile
-constexpr int F32_SMEM = (2 * 64 * FP * 2 + FK * VD + 2 * FK * FP + 128 + 4) * 4;
+constexpr int FQ = 64, FK = 64, QP = 68;  // queries and keys of a tile; padded row of a transposed tile
+constexpr int F32_THREADS = 128;
+// floats: Q [map][64][QP] (at the end the second map's O [64][132]), K and then P [map][64][QP], V [FK][VD],
+// gain, lambda
+constexpr int F32_SMEM = (2 * 64 * QP + 2 * 64 * QP + FK * VD + 128 + 4) * 4;
+static_assert(64 * 132 <= 2 * 64 * QP, "the second map's O lies over Q");
 
-// 64 queries of one row and head, all of its keys in tiles of 64; a thread holds 4 x 4 scores of each
-// map and 4 x 8 outputs of each.  Tiles lie transposed (element-major) in shared memory, so that a
-// product step reads whole vectors.
-__global__ void __launch_bounds__(256) k_diff_attention_f32(const __grid_constant__ DiffOp p) {
+// 64 queries of one row and head against its keys, 64 at a time; two warps a map.  A thread holds 8 x 8
+// scores and 8 x 16 outputs of the same rows, so that a row's running maximum and sum stay with it and
+// its seven neighbours.  Shared memory hands a lane one float a clock against four FMAs: the scores take
+// 4 FMAs a float, the outputs 5.3.  Q, K and P lie transposed (element-major), whole vectors a step; P
+// takes K's place.  Bound by FP32 arithmetic, 1536 operations a visible pair and head; two CTAs an SM.
+__global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __grid_constant__ DiffOp p) {
     extern __shared__ float fs[];
-    float *Q = fs, *K = Q + 2 * 64 * FP, *V = K + 2 * 64 * FP, *P = V + FK * VD, *gain = P + 2 * FK * FP,
-          *lambda = gain + 128;
-    const int tid = threadIdx.x, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
+    float *Q = fs, *K = Q + 2 * 64 * QP, *V = K + 2 * 64 * QP, *gain = V + FK * VD, *lambda = gain + 128;
+    const int tid = threadIdx.x, lane = tid & 31, x = tid >> 6, u = tid & 63;
     // the tiles' numbering of find_item, with 64 queries a tile
     const int b = blockIdx.x, h = blockIdx.y;
     int row = 0, n = p.n_rows;
@@ -654,123 +659,151 @@ __global__ void __launch_bounds__(256) k_diff_attention_f32(const __grid_constan
         const float c = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
         if (lane == 0) *lambda = expf(a) - expf(c) + p.lambda_init;
     }
-    if (tid < 128) gain[tid] = p.gain ? p.gain[tid] * (1.0f - p.lambda_init) : 1.0f;
+    gain[tid] = p.gain ? p.gain[tid] * (1.0f - p.lambda_init) : 1.0f;
+    // Both maps of 64 tokens, transposed: a warp takes 16 tokens by 32 bytes, whole sectors
     auto load_t = [&](float *dst, const float *src, int64_t token, int64_t head, int first, int end) {
-        // two maps x 64 rows x 16 vectors: neighbouring threads take neighbouring rows
-        for (int i = tid; i < 2 * 64 * 16; i += 256) {
-            const int r = i & 63, v4 = (i >> 6) & 15, m = i >> 10;
+#pragma unroll 4
+        for (int i = tid; i < 2 * 64 * 16; i += F32_THREADS) {
+            const int block = i >> 5, r = (i & 15) + 16 * (block & 3), v4 = ((i >> 4) & 1) + 2 * ((block >> 2) & 7), m = block >> 5;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             if (first + r < end) a = *reinterpret_cast<const float4 *>(src + (first + r) * token + m * head + 4 * v4);
-            float *d = dst + (m * 64 + 4 * v4) * FP + r;
-            d[0] = a.x, d[FP] = a.y, d[2 * FP] = a.z, d[3 * FP] = a.w;
+            float *d = dst + (m * 64 + 4 * v4) * QP + r;
+            d[0] = a.x, d[QP] = a.y, d[2 * QP] = a.z, d[3 * QP] = a.w;
         }
     };
     load_t(Q, qp, p.q_token, p.q_head, q0, ce);
-    float o[2][4][8], m[2][4], l[2][4];
+    const int ty = u >> 3, tx = u & 7;  // rows 8 ty ..; keys 4 tx .., 32 + 4 tx ..; columns 4 tx + 32 i ..
+    const float *Qm = Q + x * 64 * QP + 8 * ty;
+    float *Km = K + x * 64 * QP;
+    float2 o[8][8];
+    float m[8], l[8];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int i = 0; i < 8; ++i) {
+        m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m[x][i] = -INFINITY, l[x][i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[x][i][e] = 0.f;
-        }
+        for (int e = 0; e < 8; ++e) o[i][e] = make_float2(0.f, 0.f);
+    }
     for (int kt = k0; kt < kend; kt += FK) {
-        __syncthreads();  // the last tile's K, V and P have been used
+        __syncthreads();  // the last tile's P and V have been used
         load_t(K, kp, p.k_token, p.k_head, kt, kend);
-        for (int i = tid; i < FK * VD / 4; i += 256) {
+#pragma unroll 4
+        for (int i = tid; i < FK * VD / 4; i += F32_THREADS) {
             const int r = i >> 5, v4 = i & 31;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             if (kt + r < kend) a = *reinterpret_cast<const float4 *>(vp + (kt + r) * p.v_token + 4 * v4);
             *reinterpret_cast<float4 *>(V + r * VD + 4 * v4) = a;
         }
         __syncthreads();
+        float2 s[8][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float s[4][4] = {};
-#pragma unroll 8
-            for (int d = 0; d < 64; ++d) {
-                const float4 a = *reinterpret_cast<const float4 *>(Q + (x * 64 + d) * FP + 4 * ty);
-                const float4 c = *reinterpret_cast<const float4 *>(K + (x * 64 + d) * FP + 4 * tx);
-                const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; ++e) s[i][e] = make_float2(0.f, 0.f);
+#pragma unroll 2
+        for (int d = 0; d < 64; ++d) {
+            const float4 a0 = *reinterpret_cast<const float4 *>(Qm + d * QP), a1 = *reinterpret_cast<const float4 *>(Qm + d * QP + 4);
+            const float4 c0 = *reinterpret_cast<const float4 *>(Km + d * QP + 4 * tx),
+                         c1 = *reinterpret_cast<const float4 *>(Km + d * QP + 32 + 4 * tx);
+            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const float2 cv[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][e] = fmaf(av[i], cv[e], s[i][e]);
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = fma_f32x2(make_float2(av[i], av[i]), cv[e], s[i][e]);
+        }
+        __syncthreads();  // K has been used: P takes its place
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int qi = q0 + 8 * ty + i;
+            float v[8], mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int kj = kt + 4 * tx + (e & 3) + (e >> 2) * 32;
+                const bool seen = kj < kend && (p.window < 0 || (kj - qi <= p.window && qi - kj <= p.window));
+                v[e] = seen ? (e & 1 ? s[i][e >> 1].y : s[i][e >> 1].x) * p.scale : -INFINITY;
+                mx = fmaxf(mx, v[e]);
             }
+            for (int w = 4; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float now = fmaxf(m[i], mx), mm = now == -INFINITY ? 0.f : now;  // nothing seen yet: every P is 0
+            const float alpha = expf(m[i] - mm);
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int qi = q0 + 4 * ty + i;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int kj = kt + 4 * tx + e;
-                    const bool seen = kj < kend && (p.window < 0 || (kj - qi <= p.window && qi - kj <= p.window));
-                    s[i][e] = seen ? s[i][e] * p.scale : -INFINITY;
-                    mx = fmaxf(mx, s[i][e]);
-                }
-                for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float now = fmaxf(m[x][i], mx), mm = now == -INFINITY ? 0.f : now;
-                const float alpha = expf(m[x][i] - mm);
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[i][e] = expf(s[i][e] - mm);
-                    sum += s[i][e];
-                }
-                l[x][i] = l[x][i] * alpha + sum;
-                m[x][i] = now;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[x][i][e] *= alpha;
+            for (int e = 0; e < 8; ++e) {
+                v[e] = expf(v[e] - mm);
+                sum += v[e];
+                s[i][e >> 1] = e & 1 ? make_float2(v[e - 1], v[e]) : s[i][e >> 1];
             }
+            l[i] = l[i] * alpha + sum;
+            m[i] = now;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<float4 *>(P + (x * FK + 4 * tx + e) * FP + 4 * ty) =
-                    make_float4(s[0][e], s[1][e], s[2][e], s[3][e]);
+            for (int e = 0; e < 8; ++e) o[i][e] = make_float2(o[i][e].x * alpha, o[i][e].y * alpha);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float *dst = Km + (4 * tx + (e & 3) + (e >> 2) * 32) * QP + 8 * ty;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<float4 *>(dst + i) =
+                    e & 1 ? make_float4(s[i][e >> 1].y, s[i + 1][e >> 1].y, s[i + 2][e >> 1].y, s[i + 3][e >> 1].y)
+                          : make_float4(s[i][e >> 1].x, s[i + 1][e >> 1].x, s[i + 2][e >> 1].x, s[i + 3][e >> 1].x);
         }
         __syncthreads();
         const int keys = min(FK, kend - kt);
+#pragma unroll 2
         for (int k = 0; k < keys; ++k) {
-            const float4 v0 = *reinterpret_cast<const float4 *>(V + k * VD + 4 * tx);
-            const float4 v1 = *reinterpret_cast<const float4 *>(V + k * VD + 64 + 4 * tx);
-            const float vv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            const float4 p0 = *reinterpret_cast<const float4 *>(Km + k * QP + 8 * ty),
+                         p1 = *reinterpret_cast<const float4 *>(Km + k * QP + 8 * ty + 4);
+            const float pv[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float4 a = *reinterpret_cast<const float4 *>(P + (x * FK + k) * FP + 4 * ty);
-                const float av[4] = {a.x, a.y, a.z, a.w};
+            for (int c = 0; c < 4; ++c) {
+                const float4 v = *reinterpret_cast<const float4 *>(V + k * VD + 32 * c + 4 * tx);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[x][i][e] = fmaf(av[i], vv[e], o[x][i][e]);
+                for (int i = 0; i < 8; ++i) {
+                    o[i][2 * c] = fma_f32x2(make_float2(pv[i], pv[i]), make_float2(v.x, v.y), o[i][2 * c]);
+                    o[i][2 * c + 1] = fma_f32x2(make_float2(pv[i], pv[i]), make_float2(v.z, v.w), o[i][2 * c + 1]);
+                }
             }
         }
     }
     const float lam = *lambda;
+    float *O1 = Q;  // [64][132]
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float l0 = l[0][i], l1 = l[1][i];
-        for (int w = 8; w; w >>= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
-        }
-        const float i0 = 1.0f / l0, i1 = -lam / l1;
-        float d[8], sq = 0.f;
+    for (int i = 0; i < 8; ++i) {
+        for (int w = 4; w; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+        const float f = (x ? -lam : 1.0f) / l[i];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            d[e] = fmaf(o[1][i][e], i1, o[0][i][e] * i0);
-            sq = fmaf(d[e], d[e], sq);
+        for (int e = 0; e < 8; ++e) o[i][e] = make_float2(o[i][e].x * f, o[i][e].y * f);
+        if (x)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<float4 *>(O1 + (8 * ty + i) * 132 + 32 * c + 4 * tx) =
+                    make_float4(o[i][2 * c].x, o[i][2 * c].y, o[i][2 * c + 1].x, o[i][2 * c + 1].y);
+    }
+    __syncthreads();
+    if (x) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 a = *reinterpret_cast<const float4 *>(O1 + (8 * ty + i) * 132 + 32 * c + 4 * tx);
+            o[i][2 * c] = make_float2(o[i][2 * c].x + a.x, o[i][2 * c].y + a.y);
+            o[i][2 * c + 1] = make_float2(o[i][2 * c + 1].x + a.z, o[i][2 * c + 1].y + a.w);
         }
-        for (int w = 8; w; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq = fmaf(o[i][e].x, o[i][e].x, fmaf(o[i][e].y, o[i][e].y, sq));
+        for (int w = 4; w; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
         const float f = p.gain ? 1.0f / sqrtf(sq * (1.0f / VD) + p.eps) : 1.0f;
-        const int qi = q0 + 4 * ty + i;
+        const int qi = q0 + 8 * ty + i;
         if (qi < ce) {
             float *dst = static_cast<float *>(p.out) + qi * p.out_token + h * p.out_head;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int at = 64 * u + 4 * tx;
+            for (int c = 0; c < 4; ++c) {
+                const int at = 32 * c + 4 * tx;
                 *reinterpret_cast<float4 *>(dst + at) =
-                    make_float4(d[4 * u] * f * gain[at], d[4 * u + 1] * f * gain[at + 1], d[4 * u + 2] * f * gain[at + 2],
-                                d[4 * u + 3] * f * gain[at + 3]);
+                    make_float4(o[i][2 * c].x * f * gain[at], o[i][2 * c].y * f * gain[at + 1],
+                                o[i][2 * c + 1].x * f * gain[at + 2], o[i][2 * c + 1].y * f * gain[at + 3]);
             }
         }
     }
@@ -853,7 +886,7 @@ cudaError_t launch_diff_attention(const DiffOp &op, const DiffMaps *maps, int nu
     if (op.n_tokens <= 0 || op.n_rows <= 0) return cudaSuccess;
     if (op.qk_dtype == JD_F32) {
         const dim3 grid(op.n_tokens / FQ + op.n_rows, op.heads);
-        k_diff_attention_f32<<<grid, 256, F32_SMEM, st>>>(op);
+        k_diff_attention_f32<<<grid, F32_THREADS, F32_SMEM, st>>>(op);
         return cudaGetLastError();
     }
     const int64_t items = ((int64_t)op.n_tokens / TQ + op.n_rows) * op.heads;
