@@ -55,7 +55,7 @@ constexpr int OFF_Q = 0;                     // [item buffer][map]
 constexpr int OFF_K = OFF_Q + 4 * Q_BYTES;
 constexpr int OFF_V = OFF_K + NK * K_BYTES;
 constexpr int OFF_BAR = OFF_V + NV * V_BYTES;
-constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 4 + 2 + 1;
+constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 4 + 2 + 2;
 constexpr int OFF_F = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;
 // floats: gain[128], l[2][128], sums of squares[2][128], lambda; then the TMEM slot and a status word
 constexpr int DIFF_SMEM = OFF_F + (128 + 256 + 256 + 4) * 4 + 16 + 1024;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
     uint64_t *qfull = bars, *qfree = qfull + 2, *kfull = qfree + 2, *kfree = kfull + NK, *vfull = kfree + NK,
              *vfree = vfull + NV, *vtail = vfree + NV, *sfull = vtail + NV, *pready = sfull + 4, *pvdone = pready + 4,
-             *odone = pvdone + 4, *ofree = odone + 2;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
+             *odone = pvdone + 4, *ofree = odone + 2, *learned = ofree + 1;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
     float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128, *squares = sums + 256,
           *lambda = squares + 256;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lambda + 4);
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&pvdone[i], 1);
         }
         mbar_init(ofree, 8);
+        mbar_init(learned, 1);
         *own_status = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -318,12 +319,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
-    }
-    if (warp == 3) {
-        const float a = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
-        const float b = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
-        if (lane == 0) *lambda = expf(a) - expf(b) + p.lambda_init;
-        for (int i = lane; i < 128; i += 32) gain[i] = p.gain ? p.gain[i] * (1.0f - p.lambda_init) : 1.0f;
     }
     tc_fence_before();
     __syncthreads();
@@ -364,6 +359,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
             }
         } else if (warp == 2) {
+            // lambda and the gain, which the first item's end waits for
+            const float a = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
+            const float b = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
+            if (lane == 0) *lambda = expf(a) - expf(b) + p.lambda_init;
+            for (int i = lane; i < 128; i += 32) gain[i] = p.gain ? p.gain[i] * (1.0f - p.lambda_init) : 1.0f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(learned);
             uint32_t c = 0, tails[NV] = {};
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
                 const Item t = find_item(p, w, lane);
@@ -461,7 +463,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = tl + T_O, b_sfull = smem_u32(sfull + 2 * x), b_pready = smem_u32(pready + 2 * x);
         const float sl2 = p.scale * 1.4426950408889634f;
-        const float lam = *lambda;
         uint32_t c = 0, it = 0;  // tiles of this map and items so far
         int w = blockIdx.x;
         Item next = find_on(p, w, n_items, lane);
@@ -558,13 +559,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             next = find_on(p, w, n_items, lane);  // while the last products finish
             mbar_wait(&odone[0], it & 1, status);
             mbar_wait(&odone[1], it & 1, status);
+            if (it == 0) mbar_wait(learned, 0, status);
             ++it;
             __syncwarp();
             named_bar_sync(BAR_SUMS, 256);
             float d[64], sq = 0.f;
             if (!dead) {
                 tc_fence_after();
-                const float i0 = 1.0f / sums[r], i1 = -lam / sums[128 + r];
+                const float i0 = 1.0f / sums[r], i1 = -*lambda / sums[128 + r];
 #pragma unroll
                 for (int hc = 0; hc < 64; hc += 32) {
                     uint32_t o0[32], o1[32];
