@@ -14,13 +14,17 @@
 //   warp 2          zeroes the rows of an item's last V tile that lie past its keys: their
 //                   probabilities are 0, but 0 times what another row holds there may be NaN
 //   warps 4..7      softmax of map 0, warps 8..11 of map 1: one query row a thread
+//   warps 12..15    read-out: D, its norm and the output row, while the others are at the next item
 //
 // TMEM is full: O_0 and O_1 take 256 columns, and each map has two S tiles of 64 columns in turn, so
 // that its next scores are there while it works on these; P_x overwrites its S tile (the thread that
-// stores a row's P has read all of its S).  One S tile of 128 keys a map, whose next product must
-// wait for P V, ran at 3.08 ms on 16 rows of 8192 with three heads against TIME_LONG here.  At an item's
-// end both groups hold the same queries: group x reads columns 64 x .. 64 x + 63 of O_0 and O_1, forms
-// D, and the two halves of a row's sum of squares meet in shared memory.
+// stores a row's P has read all of its S).
+//
+// What did not pay, on 16 rows of 8192 (2.8 to 3.0 ms, with the clock under the power cap): one S tile of 128
+// keys a map, whose next product waits for P V (3.1 ms); one thread issuing the MMAs of both maps, or not elected by
+// elect.sync, at a hundred clocks an MMA (5.7 ms); two threads a row (2.7 to 3.0 ms, but 10 % slower on rows of 550);
+// asking for the next S before P is handed over (3.0 ms); a quarter of the exponentials as polynomials on the FMA pipe
+// (3.1 ms: the softmax warps are bound by issued instructions and their latencies, not by the exponential unit).
 //
 // Bound: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
 // exponentials a clock and SM, 0.094 and 0.125 clocks.
@@ -55,23 +59,20 @@ constexpr int OFF_Q = 0;                     // [item buffer][map]
 constexpr int OFF_K = OFF_Q + 4 * Q_BYTES;
 constexpr int OFF_V = OFF_K + NK * K_BYTES;
 constexpr int OFF_BAR = OFF_V + NV * V_BYTES;
-constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 4 + 2 + 2;
+constexpr int NBAR = 2 + 2 + 2 * NK + 3 * NV + 3 * 4 + 2 + 2 + 1;
 constexpr int OFF_F = OFF_BAR + ((NBAR * 8 + 15) / 16) * 16;
-// floats: gain[128], l[2][128], sums of squares[2][128], lambda; then the TMEM slot and a status word
-constexpr int DIFF_SMEM = OFF_F + (128 + 256 + 256 + 4) * 4 + 16 + 1024;
+// floats: gain[128], row sums [item % 2][map][128]; then the TMEM slot and a status word
+constexpr int DIFF_SMEM = OFF_F + (128 + 2 * 256) * 4 + 16 + 1024;
 static_assert(DIFF_SMEM <= 227 * 1024, "differential attention shared memory");
 constexpr uint32_t T_S = 0, T_O = 256;
 constexpr float kLazy = 8.0f;                // log2 headroom before a running max is moved: P <= 2^8
-#ifndef DP
-#define DP 0
-#endif
-constexpr int POLY_OF_8 = DP;
-constexpr int THREADS = 12 * 32;
-// As in the global attention: the compiled count (checked on the host), what warp group 0 keeps and
-// what each softmax group takes.
-constexpr int REGS = 168, REGS_LOW = 120, REGS_HIGH = 192;
-static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= THREADS * REGS, "register split");
-constexpr int BAR_SUMS = 1, BAR_SQUARES = 2;  // named barriers of the two softmax groups
+constexpr int THREADS = 16 * 32;
+// The launch gives every thread REGS registers (the compiled count, checked on the host before the first
+// launch: a warp group asking for more than the launch holds would wait for ever); the warp groups of the
+// roles and of the read-out give up some, which the softmax groups take.
+constexpr int REGS = 128, REGS_ROLES = 72, REGS_READOUT = 104, REGS_SOFTMAX = 160;
+constexpr int BAR_GAIN = 1;  // named barrier of the read-out warps
+static_assert(128 * (REGS_ROLES + REGS_READOUT) + 256 * REGS_SOFTMAX <= THREADS * REGS, "register split");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -96,40 +97,6 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
         "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
-// 2^x for a pair on the FMA and integer pipes.  x = j + f, j = round(x): adding 1.5 * 2^23 leaves j in
-// the low mantissa bits; 2^f on [-1/2, 1/2] is the polynomial of least maximum relative error (Remez
-// exchange): degree 4 off by 2.6e-6, degree 5 by 7.5e-8; j is added to the exponent.  Below -126 the
-// sum of exponents turns negative, which is held at 0; NaN stays NaN or becomes infinite.
-template <int DEGREE>
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
-    x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
-    const float2 t = add_f32x2(x, make_float2(12582912.f, 12582912.f));
-    const float2 j = add_f32x2(t, make_float2(-12582912.f, -12582912.f));
-    const float2 f = fma_f32x2(j, make_float2(-1.f, -1.f), x);
-    auto both = [](float c) { return make_float2(c, c); };
-    float2 q;
-    if (DEGREE == 4) {
-        q = fma_f32x2(f, both(0.009570102207362652f), both(0.05591785907745361f));
-        q = fma_f32x2(q, f, both(0.240247443318367f));
-        q = fma_f32x2(q, f, both(0.6931217908859253f));
-        q = fma_f32x2(q, f, both(0.9999992847442627f));
-    } else {
-        q = fma_f32x2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
-        q = fma_f32x2(q, f, both(0.05550713092088699f));
-        q = fma_f32x2(q, f, both(0.24022120237350464f));
-        q = fma_f32x2(q, f, both(0.6931469440460205f));
-        q = fma_f32x2(q, f, both(1.0000001192092896f));
-    }
-    return make_float2(__int_as_float(max(__float_as_int(q.x) + (__float_as_int(t.x) << 23), 0)),
-                       __int_as_float(max(__float_as_int(q.y) + (__float_as_int(t.y) << 23), 0)));
 }
 
 __device__ __forceinline__ void tma_load_heads(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int head, int token) {
@@ -280,10 +247,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
     uint64_t *qfull = bars, *qfree = qfull + 2, *kfull = qfree + 2, *kfree = kfull + NK, *vfull = kfree + NK,
              *vfree = vfull + NV, *vtail = vfree + NV, *sfull = vtail + NV, *pready = sfull + 4, *pvdone = pready + 4,
-             *odone = pvdone + 4, *ofree = odone + 2, *learned = ofree + 1;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
-    float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128, *squares = sums + 256,
-          *lambda = squares + 256;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(lambda + 4);
+             *odone = pvdone + 4, *summed = odone + 2, *ofree = summed + 2;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
+    float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sums + 512);
     unsigned *own_status = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -301,14 +267,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&qfull[i], 1);
             mbar_init(&qfree[i], 2);
             mbar_init(&odone[i], 1);
+            mbar_init(&summed[i], 8);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pready[i], 4);
             mbar_init(&pvdone[i], 1);
         }
-        mbar_init(ofree, 8);
-        mbar_init(learned, 1);
+        mbar_init(ofree, 4);
         *own_status = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -326,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     unsigned *status = p.status ? p.status : own_status;
     if (warp < 4) {  // warp group 0: producers, MMA issue, the tail of V
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_LOW));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
         if (warp == 0) {
             uint32_t c = 0, it = 0;  // tiles, items
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
@@ -359,13 +325,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
             }
         } else if (warp == 2) {
-            // lambda and the gain, which the first item's end waits for
-            const float a = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
-            const float b = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
-            if (lane == 0) *lambda = expf(a) - expf(b) + p.lambda_init;
-            for (int i = lane; i < 128; i += 32) gain[i] = p.gain ? p.gain[i] * (1.0f - p.lambda_init) : 1.0f;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(learned);
             uint32_t c = 0, tails[NV] = {};
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
                 const Item t = find_item(p, w, lane);
@@ -422,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint32_t b = c & 1, s = c % NV;
                         wait(b_vfull + 8 * s, (c / NV) & 1, status);
                         wait(b_pready + 8 * b, (c >> 1) & 1, status);
-                        if (j == 0 && it > 0) wait(smem_u32(ofree), (it - 1) & 1, status);
+                        if (j == 0 && it > 0) wait(smem_u32(ofree), (it - 1) & 1, status);  // the last O has been read
                         tc_fence_after();
                         const uint32_t o = tmem + T_O + VD * x, pt = tmem + T_S + 2 * TK * x + TK * b,
                                        v = v_lo + s * (V_BYTES >> 4);
@@ -456,8 +415,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 now = next;
             }
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_HIGH));
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int x = (warp - 4) >> 2;         // this group's map
         const int r = (warp & 3) * 32 + lane;  // query row inside the tile = TMEM lane
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -468,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Item next = find_on(p, w, n_items, lane);
         while (next.on) {
             const Item t = next;
+            next = find_on(p, w, n_items, lane);
             const int qi = t.q0 + r;
             const bool dead = t.q0 + (warp & 3) * 32 >= t.ce;  // no row of this warp: it only keeps the order
             // keys this row sees, from the tile's first on: [a, b)
@@ -536,8 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const float2 xv =
                             fma_f32x2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
                                       make_float2(sl2, sl2), make_float2(-mm, -mm));
-                        const float2 pv = ((e >> 1) & 7) < POLY_OF_8 ? exp2_poly<SPLIT ? 5 : 4>(xv)
-                                                                     : make_float2(exp2_fast(xv.x), exp2_fast(xv.y));
+                        const float2 pv = make_float2(exp2_fast(xv.x), exp2_fast(xv.y));
                         ls[(e >> 1) & 3] = add_f32x2(ls[(e >> 1) & 3], pv);
                         pk[e >> 1] = pack_p<V16>(pv.x, pv.y);
                         if (SPLIT) {
@@ -554,61 +513,99 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) arrive(b_pready + 8 * (c & 1));
             }
-            // Both maps' sums, then this group's half of the columns of both O
-            sums[128 * x + r] = l;
-            next = find_on(p, w, n_items, lane);  // while the last products finish
-            mbar_wait(&odone[0], it & 1, status);
-            mbar_wait(&odone[1], it & 1, status);
-            if (it == 0) mbar_wait(learned, 0, status);
+            sums[256 * (it & 1) + 128 * x + r] = l;
+            __syncwarp();
+            if (lane == 0) arrive(smem_u32(&summed[it & 1]));
             ++it;
+        }
+    } else {
+        // Read-out, one row a thread: D in two passes over both O (its norm, then its values: all of D would not
+        // fit the registers), while the softmax groups are at the next item: they may finish it, so the sums of two
+        // items are kept, but not the one behind it, whose S follow the next O, which waits for this read-out.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_READOUT));
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + T_O;
+        const float la = warp_sum(p.lq1[lane] * p.lk1[lane] + p.lq1[lane + 32] * p.lk1[lane + 32]);
+        const float lb = warp_sum(p.lq2[lane] * p.lk2[lane] + p.lq2[lane + 32] * p.lk2[lane + 32]);
+        const float lam = expf(la) - expf(lb) + p.lambda_init;
+        gain[r] = p.gain ? p.gain[r] * (1.0f - p.lambda_init) : 1.0f;
+        named_bar_sync(BAR_GAIN, 128);
+        const bool out16 = p.qk_dtype == JD_F16;
+        uint32_t it = 0;
+        int w = blockIdx.x;
+        Item next = find_on(p, w, n_items, lane);
+        while (next.on) {
+            const Item t = next;
+            next = find_on(p, w, n_items, lane);
+            wait(smem_u32(&summed[it & 1]), (it >> 1) & 1, status);
+            wait(smem_u32(&odone[0]), it & 1, status);
+            wait(smem_u32(&odone[1]), it & 1, status);
             __syncwarp();
-            named_bar_sync(BAR_SUMS, 256);
-            float d[64], sq = 0.f;
-            if (!dead) {
+            const int qi = t.q0 + r;
+            if (t.q0 + (warp & 3) * 32 < t.ce) {
                 tc_fence_after();
-                const float i0 = 1.0f / sums[r], i1 = -*lambda / sums[128 + r];
+                const float *sum = sums + 256 * (it & 1) + r;
+                const float i0 = 1.0f / sum[0], i1 = -lam / sum[128];
+                float f = 1.0f;
+                if (p.gain) {
+                    float sq = 0.f;
+#pragma unroll 1
+                    for (int e0 = 0; e0 < VD; e0 += 32) {
+                        uint32_t o0[32], o1[32];
+                        tmem_ld32(to + e0, o0);
+                        tmem_ld32(to + VD + e0, o1);
+                        tmem_ld_wait();
 #pragma unroll
-                for (int hc = 0; hc < 64; hc += 32) {
+                        for (int e = 0; e < 32; ++e) {
+                            const float d = fmaf(__uint_as_float(o1[e]), i1, __uint_as_float(o0[e]) * i0);
+                            sq = fmaf(d, d, sq);
+                        }
+                    }
+                    f = rsqrtf(sq * (1.0f / VD) + p.eps);
+                }
+                const float f0 = f * i0, f1 = f * i1;
+                uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (qi * p.out_token + t.h * p.out_head);
+#pragma unroll 1
+                for (int e0 = 0; e0 < VD; e0 += 32) {
                     uint32_t o0[32], o1[32];
-                    tmem_ld32(to + 64 * x + hc, o0);
-                    tmem_ld32(to + VD + 64 * x + hc, o1);
+                    tmem_ld32(to + e0, o0);
+                    tmem_ld32(to + VD + e0, o1);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        d[hc + e] = fmaf(__uint_as_float(o1[e]), i1, __uint_as_float(o0[e]) * i0);
-                        sq = fmaf(d[hc + e], d[hc + e], sq);
+                    if (e0 == VD - 32) {  // both O have been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(smem_u32(ofree));
                     }
+                    if (qi < t.ce) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float4 g = *reinterpret_cast<const float4 *>(&gain[e0 + e + 2 * i]);
+                                float v[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    v[k] = fmaf(__uint_as_float(o1[e + 2 * i + k]), f1, __uint_as_float(o0[e + 2 * i + k]) * f0);
+                                v[0] *= g.x, v[1] *= g.y, v[2] *= g.z, v[3] *= g.w;
+                                u[i] = out16 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]);
+                                u[i + 1] = out16 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]);
+                            }
+                            if (p.out32) {  // a row a thread: 32-byte stores fill whole sectors
+                                st_global_v8(dst + 2 * (e0 + e), u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + 2 * (e0 + e)) = make_uint4(u[0], u[1], u[2], u[3]);
+                                *reinterpret_cast<uint4 *>(dst + 2 * (e0 + e) + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                            }
+                        }
+                    }
+                    __syncwarp();  // whole warps read TMEM
                 }
-                tc_fence_before();
+            } else if (lane == 0) {
+                arrive(smem_u32(ofree));
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(ofree);
-            squares[128 * x + r] = sq;
-            __syncwarp();
-            named_bar_sync(BAR_SQUARES, 256);
-            if (qi < t.ce) {
-                const float f = p.gain ? rsqrtf((squares[r] + squares[128 + r]) * (1.0f / VD) + p.eps) : 1.0f;
-                uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (qi * p.out_token + t.h * p.out_head + 64 * x);
-                const bool out16 = p.qk_dtype == JD_F16;
-#pragma unroll
-                for (int e = 0; e < 64; e += 16) {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float4 g = *reinterpret_cast<const float4 *>(&gain[64 * x + e + 2 * i]);
-                        const float v[4] = {d[e + 2 * i] * f * g.x, d[e + 2 * i + 1] * f * g.y, d[e + 2 * i + 2] * f * g.z,
-                                            d[e + 2 * i + 3] * f * g.w};
-                        u[i] = out16 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]);
-                        u[i + 1] = out16 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]);
-                    }
-                    if (p.out32) {  // a row a thread: 32-byte stores fill whole sectors
-                        st_global_v8(dst + 2 * e, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
-                    } else {
-                        *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(u[0], u[1], u[2], u[3]);
-                        *reinterpret_cast<uint4 *>(dst + 2 * e + 16) = make_uint4(u[4], u[5], u[6], u[7]);
-                    }
-                }
-            }
+            ++it;
         }
     }
     __syncthreads();
