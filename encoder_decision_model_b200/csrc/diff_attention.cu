@@ -191,29 +191,27 @@ struct Item {
 
 // Work item w: head w % heads of query tile w / heads.  Tile numbers are spread so that no table is
 // needed: row r's tiles start at cu[r] / 128 + r, which leaves every row room for all of its tiles; a
-// number past a row's last tile is an empty item.  The row is found 32 probes at a time; all lanes
-// of a warp call this.
-__device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
+// number past a row's last tile is an empty item.  A role's items ascend, so its search goes on from the
+// last row, 31 rows a look (one load, and the row's ends by shuffle).  All lanes of a warp call this.
+__device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane, int &lo) {
     Item t;
     const int b = w / p.heads;
     t.h = w - b * p.heads;
-    int lo = 0, n = p.n_rows;
-    t.on = true;
-    while (n > 1) {
-        const int step = (n + 31) >> 5, at = lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, at < n && (p.cu[lo + at] >> 7) + lo + at <= b);
-        if (!(below & 1u)) {
-            t.on = false;
-            break;
+    for (;;) {
+        const int at = lo + lane, v = p.cu[min(at, p.n_rows)];
+        const unsigned below = __ballot_sync(0xffffffffu, at < p.n_rows && (v >> 7) + at <= b);
+        if (below == 0xffffffffu && lo + 32 < p.n_rows) {
+            lo += 31;
+            continue;
         }
-        const int k = 31 - __clz(below);
-        lo += k * step;
-        n = min(step, n - k * step);
+        const int k = min(31 - __clz(below | 1u), 30);
+        t.cs = max(__shfl_sync(0xffffffffu, v, k), 0);
+        t.ce = min(__shfl_sync(0xffffffffu, v, k + 1), p.n_tokens);
+        lo += k;
+        break;
     }
-    t.cs = max(p.cu[lo], 0);
-    t.ce = min(p.cu[lo + 1], p.n_tokens);
     t.q0 = t.cs + (b - (t.cs >> 7) - lo) * TQ;
-    t.on = t.on && t.q0 >= t.cs && t.q0 < t.ce;
+    t.on = t.q0 >= t.cs && t.q0 < t.ce;
     t.k0 = p.window < 0 ? t.cs : max(t.cs, t.q0 - p.window);
     t.kend = p.window < 0 ? t.ce : min(t.ce, min(t.q0 + TQ, t.ce) + p.window);
     t.nt = (t.kend - t.k0 + TK - 1) / TK;
@@ -221,10 +219,17 @@ __device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane) {
 }
 
 // The next item that is not empty, from w on; w moves past it.
-__device__ __forceinline__ Item find_on(const DiffOp &p, int &w, int n_items, int lane) {
+__device__ __forceinline__ Item find_on(const DiffOp &p, int &w, int n_items, int lane, int &lo) {
     Item t;
-    for (t.on = false; w < n_items && !t.on; w += gridDim.x) t = find_item(p, w, lane);
+    for (t.on = false; w < n_items && !t.on; w += gridDim.x) t = find_item(p, w, lane, lo);
     return t;
+}
+
+// Bits a .. b - 1 of a word.
+__device__ __forceinline__ uint32_t bits(int a, int b) {
+    const uint32_t from = a <= 0 ? 0xffffffffu : (a < 32 ? 0xffffffffu << a : 0u);
+    const uint32_t to = b >= 32 ? 0xffffffffu : (b > 0 ? (1u << b) - 1u : 0u);
+    return from & to;
 }
 
 template <bool V16>  // V16: FP16 values, else BF16
@@ -291,12 +296,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     unsigned *status = p.status ? p.status : own_status;
+    int row = 0;  // where this warp's search for items has got to
     if (warp < 4) {  // warp group 0: producers, MMA issue, the tail of V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
         if (warp == 0) {
             uint32_t c = 0, it = 0;  // tiles, items
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-                const Item t = find_item(p, w, lane);
+                const Item t = find_item(p, w, lane, row);
                 if (!t.on) continue;
                 if (lane == 0) {
                     const int vh = t.h / (p.heads / p.kv_heads);
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 2) {
             uint32_t c = 0, tails[NV] = {};
             for (int w = blockIdx.x; w < n_items; w += gridDim.x) {
-                const Item t = find_item(p, w, lane);
+                const Item t = find_item(p, w, lane, row);
                 if (!t.on) continue;
                 c += t.nt;
                 const int valid = t.in_last();
@@ -369,9 +375,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             };
             // S products run up to two tiles ahead of the PV products, into the next item if it has come to that
             int w = blockIdx.x, ahead = 0;  // ahead: S products of the current item issued so far
-            Item now = find_on(p, w, n_items, lane);
+            Item now = find_on(p, w, n_items, lane, row);
             while (now.on) {
-                const Item next = find_on(p, w, n_items, lane);
+                const Item next = find_on(p, w, n_items, lane, row);
                 if (elect_one()) {
                     const uint32_t buf = it & 1;
                     if (ahead == 0) wait(smem_u32(&qfull[buf]), (it >> 1) & 1, status);
@@ -424,10 +430,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float sl2 = p.scale * 1.4426950408889634f;
         uint32_t c = 0, it = 0;  // tiles of this map and items so far
         int w = blockIdx.x;
-        Item next = find_on(p, w, n_items, lane);
+        Item next = find_on(p, w, n_items, lane, row);
         while (next.on) {
             const Item t = next;
-            next = find_on(p, w, n_items, lane);
+            next = find_on(p, w, n_items, lane, row);
             const int qi = t.q0 + r;
             const bool dead = t.q0 + (warp & 3) * 32 >= t.ce;  // no row of this warp: it only keeps the order
             // keys this row sees, from the tile's first on: [a, b)
@@ -453,9 +459,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                     tmem_ld_wait();
                     if (__any_sync(0xffffffffu, a > 0 || b < TK)) {
+                        const uint32_t seen[2] = {bits(a, b), bits(a - 32, b - 32)};
 #pragma unroll
                         for (int e = 0; e < TK; ++e)
-                            if (e < a || e >= b) sv[e] = __float_as_uint(-INFINITY);
+                            if (!(seen[e >> 5] & (1u << (e & 31)))) sv[e] = __float_as_uint(-INFINITY);
                     }
                     float m4[4];
 #pragma unroll
@@ -533,10 +540,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool out16 = p.qk_dtype == JD_F16;
         uint32_t it = 0;
         int w = blockIdx.x;
-        Item next = find_on(p, w, n_items, lane);
+        Item next = find_on(p, w, n_items, lane, row);
         while (next.on) {
             const Item t = next;
-            next = find_on(p, w, n_items, lane);
+            next = find_on(p, w, n_items, lane, row);
             wait(smem_u32(&summed[it & 1]), (it >> 1) & 1, status);
             wait(smem_u32(&odone[0]), it & 1, status);
             wait(smem_u32(&odone[1]), it & 1, status);
