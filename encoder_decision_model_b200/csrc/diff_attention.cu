@@ -169,6 +169,14 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, unsigned *st
         }
     }
 }
+// 32 lanes x 16 columns of 32-bit TMEM cells -> 16 registers a thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
 // One lane of a converged warp; the compiler knows that only one thread goes on.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -538,6 +546,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         gain[r] = p.gain ? p.gain[r] * (1.0f - p.lambda_init) : 1.0f;
         named_bar_sync(BAR_GAIN, 128);
         const bool out16 = p.qk_dtype == JD_F16;
+        // elements e, e + 1 of a O_0 + b O_1
+        auto both = [](const uint32_t (&x)[16], const uint32_t (&y)[16], int e, float a, float b) {
+            const float2 z = make_float2(__uint_as_float(x[e]) * a, __uint_as_float(x[e + 1]) * a);
+            return fma_f32x2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), make_float2(b, b), z);
+        };
         uint32_t it = 0;
         int w = blockIdx.x;
         Item next = find_on(p, w, n_items, lane, row);
@@ -554,59 +567,63 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float *sum = sums + 256 * (it & 1) + r;
                 const float i0 = 1.0f / sum[0], i1 = -lam / sum[128];
                 float f = 1.0f;
+                // Sixteen columns of both O at a time, the next ones asked for before these are worked on.
+                uint32_t o0[2][16], o1[2][16];
+                auto ask = [&](int e0, int k) {
+                    tmem_ld16(to + e0, o0[k]);
+                    tmem_ld16(to + VD + e0, o1[k]);
+                };
+                ask(0, 0);
                 if (p.gain) {
-                    float sq = 0.f;
+                    float2 sq = make_float2(0.f, 0.f);
 #pragma unroll 1
                     for (int e0 = 0; e0 < VD; e0 += 32) {
-                        uint32_t o0[32], o1[32];
-                        tmem_ld32(to + e0, o0);
-                        tmem_ld32(to + VD + e0, o1);
-                        tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float d = fmaf(__uint_as_float(o1[e]), i1, __uint_as_float(o0[e]) * i0);
-                            sq = fmaf(d, d, sq);
+                        for (int k = 0; k < 2; ++k) {
+                            tmem_ld_wait();
+                            ask((e0 + 16 * k + 16) & (VD - 1), k ^ 1);  // (behind the last the first again)
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float2 d = both(o0[k], o1[k], e, i0, i1);
+                                sq = fma_f32x2(d, d, sq);
+                            }
                         }
                     }
-                    f = rsqrtf(sq * (1.0f / VD) + p.eps);
+                    f = rsqrtf((sq.x + sq.y) * (1.0f / VD) + p.eps);
                 }
                 const float f0 = f * i0, f1 = f * i1;
                 uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (qi * p.out_token + t.h * p.out_head);
 #pragma unroll 1
                 for (int e0 = 0; e0 < VD; e0 += 32) {
-                    uint32_t o0[32], o1[32];
-                    tmem_ld32(to + e0, o0);
-                    tmem_ld32(to + VD + e0, o1);
-                    tmem_ld_wait();
-                    if (e0 == VD - 32) {  // both O have been read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive(smem_u32(ofree));
-                    }
-                    if (qi < t.ce) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {
-                            uint32_t u[8];
+                    for (int k = 0; k < 2; ++k) {
+                        const int at = e0 + 16 * k;
+                        tmem_ld_wait();
+                        if (at < VD - 16) {
+                            ask(at + 16, k ^ 1);
+                        } else {  // both O have been read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive(smem_u32(ofree));
+                        }
+                        uint32_t u[8];
 #pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float4 g = *reinterpret_cast<const float4 *>(&gain[e0 + e + 2 * i]);
-                                float v[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    v[k] = fmaf(__uint_as_float(o1[e + 2 * i + k]), f1, __uint_as_float(o0[e + 2 * i + k]) * f0);
-                                v[0] *= g.x, v[1] *= g.y, v[2] *= g.z, v[3] *= g.w;
-                                u[i] = out16 ? pack_f16x2(v[0], v[1]) : pack_bf16x2(v[0], v[1]);
-                                u[i + 1] = out16 ? pack_f16x2(v[2], v[3]) : pack_bf16x2(v[2], v[3]);
-                            }
+                        for (int i = 0; i < 8; i += 2) {
+                            const float4 g = *reinterpret_cast<const float4 *>(&gain[at + 2 * i]);
+                            float2 v = both(o0[k], o1[k], 2 * i, f0, f1), v2 = both(o0[k], o1[k], 2 * i + 2, f0, f1);
+                            u[i] = out16 ? pack_f16x2(v.x * g.x, v.y * g.y) : pack_bf16x2(v.x * g.x, v.y * g.y);
+                            u[i + 1] = out16 ? pack_f16x2(v2.x * g.z, v2.y * g.w) : pack_bf16x2(v2.x * g.z, v2.y * g.w);
+                        }
+                        if (qi < t.ce) {
                             if (p.out32) {  // a row a thread: 32-byte stores fill whole sectors
-                                st_global_v8(dst + 2 * (e0 + e), u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+                                st_global_v8(dst + 2 * at, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
                             } else {
-                                *reinterpret_cast<uint4 *>(dst + 2 * (e0 + e)) = make_uint4(u[0], u[1], u[2], u[3]);
-                                *reinterpret_cast<uint4 *>(dst + 2 * (e0 + e) + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                                *reinterpret_cast<uint4 *>(dst + 2 * at) = make_uint4(u[0], u[1], u[2], u[3]);
+                                *reinterpret_cast<uint4 *>(dst + 2 * at + 16) = make_uint4(u[4], u[5], u[6], u[7]);
                             }
                         }
+                        __syncwarp();  // whole warps read TMEM
                     }
-                    __syncwarp();  // whole warps read TMEM
                 }
             } else if (lane == 0) {
                 arrive(smem_u32(ofree));
