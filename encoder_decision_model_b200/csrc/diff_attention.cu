@@ -641,35 +641,37 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ FP32
 
-constexpr int FQ = 64, FK = 64, QP = 68;  // queries and keys of a tile; padded row of a transposed tile
+constexpr int FK = 64, QP = 68;  // keys of a tile; padded row of a transposed tile
 constexpr int F32_THREADS = 128;
-// floats: Q [map][64][QP] (at the end the second map's O [64][132]), K and then P [map][64][QP], V [FK][VD],
+// floats: Q [map][64][QP] (at the end the second map's O [8 R][132]), K and then P [map][64][QP], V [FK][VD],
 // gain, lambda
 constexpr int F32_SMEM = (2 * 64 * QP + 2 * 64 * QP + FK * VD + 128 + 4) * 4;
 static_assert(64 * 132 <= 2 * 64 * QP, "the second map's O lies over Q");
 
-// 64 queries of one row and head against its keys, 64 at a time; two warps a map.  A thread holds 8 x 8
-// scores and 8 x 16 outputs of the same rows, so that a row's running maximum and sum stay with it and
-// its seven neighbours.  Shared memory hands a lane one float a clock against four FMAs: the scores take
-// 4 FMAs a float, the outputs 5.3.  Q, K and P lie transposed (element-major), whole vectors a step; P
+// 8 R queries of one row and head against its keys, 64 at a time; two warps a map.  A thread holds R x 8
+// scores and R x 16 outputs of the same rows, so that a row's running maximum and sum stay with it and
+// its seven neighbours.  Shared memory hands a lane one float a clock against four FMAs: with R = 8 the
+// scores take 4 FMAs a float, the outputs 5.3; R = 4 is for calls too small to fill the SMs with that.  Q, K and P lie transposed (element-major), whole vectors a step; P
 // takes K's place.  Bound by FP32 arithmetic, 1536 operations a visible pair and head; two CTAs an SM.
+template <int R>
 __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __grid_constant__ DiffOp p) {
+    constexpr int FQ = 8 * R, SHIFT = R == 8 ? 6 : 5;
     extern __shared__ float fs[];
     float *Q = fs, *K = Q + 2 * 64 * QP, *V = K + 2 * 64 * QP, *gain = V + FK * VD, *lambda = gain + 128;
     const int tid = threadIdx.x, lane = tid & 31, x = tid >> 6, u = tid & 63;
-    // the tiles' numbering of find_item, with 64 queries a tile
+    // the tiles' numbering of find_item, with FQ queries a tile
     const int b = blockIdx.x, h = blockIdx.y;
     int row = 0, n = p.n_rows;
     while (n > 1) {
         const int step = (n + 31) >> 5, at = lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, at < n && (p.cu[row + at] >> 6) + row + at <= b);
+        const unsigned below = __ballot_sync(0xffffffffu, at < n && (p.cu[row + at] >> SHIFT) + row + at <= b);
         if (!(below & 1u)) return;
         const int k = 31 - __clz(below);
         row += k * step;
         n = min(step, n - k * step);
     }
     const int cs = max(p.cu[row], 0), ce = min(p.cu[row + 1], p.n_tokens);
-    const int q0 = cs + (b - (cs >> 6) - row) * FQ;
+    const int q0 = cs + (b - (cs >> SHIFT) - row) * FQ;
     if (q0 < cs || q0 >= ce) return;
     const int k0 = p.window < 0 ? cs : max(cs, q0 - p.window);
     const int kend = p.window < 0 ? ce : min(ce, min(q0 + FQ, ce) + p.window);
@@ -683,32 +685,34 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
         if (lane == 0) *lambda = expf(a) - expf(c) + p.lambda_init;
     }
     gain[tid] = p.gain ? p.gain[tid] * (1.0f - p.lambda_init) : 1.0f;
-    // Both maps of 64 tokens, transposed: a warp takes 16 tokens by 32 bytes, whole sectors
-    auto load_t = [&](float *dst, const float *src, int64_t token, int64_t head, int first, int end) {
+    // Both maps of `rows` tokens, transposed: a warp takes 16 tokens by 32 bytes, whole sectors
+    auto load_t = [&](float *dst, int rows, const float *src, int64_t token, int64_t head, int first, int end) {
+        const int groups = rows >> 4;
 #pragma unroll 4
-        for (int i = tid; i < 2 * 64 * 16; i += F32_THREADS) {
-            const int block = i >> 5, r = (i & 15) + 16 * (block & 3), v4 = ((i >> 4) & 1) + 2 * ((block >> 2) & 7), m = block >> 5;
+        for (int i = tid; i < 2 * 16 * rows; i += F32_THREADS) {
+            const int block = i >> 5, r = (i & 15) + 16 * (block & (groups - 1)),
+                      v4 = ((i >> 4) & 1) + 2 * (block / groups & 7), m = block / groups >> 3;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             if (first + r < end) a = *reinterpret_cast<const float4 *>(src + (first + r) * token + m * head + 4 * v4);
             float *d = dst + (m * 64 + 4 * v4) * QP + r;
             d[0] = a.x, d[QP] = a.y, d[2 * QP] = a.z, d[3 * QP] = a.w;
         }
     };
-    load_t(Q, qp, p.q_token, p.q_head, q0, ce);
-    const int ty = u >> 3, tx = u & 7;  // rows 8 ty ..; keys 4 tx .., 32 + 4 tx ..; columns 4 tx + 32 i ..
-    const float *Qm = Q + x * 64 * QP + 8 * ty;
+    load_t(Q, FQ, qp, p.q_token, p.q_head, q0, ce);
+    const int ty = u >> 3, tx = u & 7;  // rows R ty ..; keys 4 tx .., 32 + 4 tx ..; columns 4 tx + 32 i ..
+    const float *Qm = Q + x * 64 * QP + R * ty;
     float *Km = K + x * 64 * QP;
-    float2 o[8][8];
-    float m[8], l[8];
+    float2 o[R][8];
+    float m[R], l[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[i][e] = make_float2(0.f, 0.f);
     }
     for (int kt = k0; kt < kend; kt += FK) {
         __syncthreads();  // the last tile's P and V have been used
-        load_t(K, kp, p.k_token, p.k_head, kt, kend);
+        load_t(K, FK, kp, p.k_token, p.k_head, kt, kend);
 #pragma unroll 4
         for (int i = tid; i < FK * VD / 4; i += F32_THREADS) {
             const int r = i >> 5, v4 = i & 31;
@@ -717,27 +721,28 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
             *reinterpret_cast<float4 *>(V + r * VD + 4 * v4) = a;
         }
         __syncthreads();
-        float2 s[8][4];
+        float2 s[R][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[i][e] = make_float2(0.f, 0.f);
 #pragma unroll 2
         for (int d = 0; d < 64; ++d) {
-            const float4 a0 = *reinterpret_cast<const float4 *>(Qm + d * QP), a1 = *reinterpret_cast<const float4 *>(Qm + d * QP + 4);
+            float av[R];
+#pragma unroll
+            for (int i = 0; i < R; i += 4) *reinterpret_cast<float4 *>(&av[i]) = *reinterpret_cast<const float4 *>(Qm + d * QP + i);
             const float4 c0 = *reinterpret_cast<const float4 *>(Km + d * QP + 4 * tx),
                          c1 = *reinterpret_cast<const float4 *>(Km + d * QP + 32 + 4 * tx);
-            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
             const float2 cv[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][e] = fma_f32x2(make_float2(av[i], av[i]), cv[e], s[i][e]);
         }
         __syncthreads();  // K has been used: P takes its place
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int qi = q0 + 8 * ty + i;
+        for (int i = 0; i < R; ++i) {
+            const int qi = q0 + R * ty + i;
             float v[8], mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -763,9 +768,9 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float *dst = Km + (4 * tx + (e & 3) + (e >> 2) * 32) * QP + 8 * ty;
+            float *dst = Km + (4 * tx + (e & 3) + (e >> 2) * 32) * QP + R * ty;
 #pragma unroll
-            for (int i = 0; i < 8; i += 4)
+            for (int i = 0; i < R; i += 4)
                 *reinterpret_cast<float4 *>(dst + i) =
                     e & 1 ? make_float4(s[i][e >> 1].y, s[i + 1][e >> 1].y, s[i + 2][e >> 1].y, s[i + 3][e >> 1].y)
                           : make_float4(s[i][e >> 1].x, s[i + 1][e >> 1].x, s[i + 2][e >> 1].x, s[i + 3][e >> 1].x);
@@ -774,14 +779,15 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
         const int keys = min(FK, kend - kt);
 #pragma unroll 2
         for (int k = 0; k < keys; ++k) {
-            const float4 p0 = *reinterpret_cast<const float4 *>(Km + k * QP + 8 * ty),
-                         p1 = *reinterpret_cast<const float4 *>(Km + k * QP + 8 * ty + 4);
-            const float pv[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+            float pv[R];
+#pragma unroll
+            for (int i = 0; i < R; i += 4)
+                *reinterpret_cast<float4 *>(&pv[i]) = *reinterpret_cast<const float4 *>(Km + k * QP + R * ty + i);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float4 v = *reinterpret_cast<const float4 *>(V + k * VD + 32 * c + 4 * tx);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < R; ++i) {
                     o[i][2 * c] = fma_f32x2(make_float2(pv[i], pv[i]), make_float2(v.x, v.y), o[i][2 * c]);
                     o[i][2 * c + 1] = fma_f32x2(make_float2(pv[i], pv[i]), make_float2(v.z, v.w), o[i][2 * c + 1]);
                 }
@@ -792,7 +798,7 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
     float *O1 = Q;  // [64][132]
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         for (int w = 4; w; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
         const float f = (x ? -lam : 1.0f) / l[i];
 #pragma unroll
@@ -800,17 +806,17 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
         if (x)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<float4 *>(O1 + (8 * ty + i) * 132 + 32 * c + 4 * tx) =
+                *reinterpret_cast<float4 *>(O1 + (R * ty + i) * 132 + 32 * c + 4 * tx) =
                     make_float4(o[i][2 * c].x, o[i][2 * c].y, o[i][2 * c + 1].x, o[i][2 * c + 1].y);
     }
     __syncthreads();
     if (x) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         float sq = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 a = *reinterpret_cast<const float4 *>(O1 + (8 * ty + i) * 132 + 32 * c + 4 * tx);
+            const float4 a = *reinterpret_cast<const float4 *>(O1 + (R * ty + i) * 132 + 32 * c + 4 * tx);
             o[i][2 * c] = make_float2(o[i][2 * c].x + a.x, o[i][2 * c].y + a.y);
             o[i][2 * c + 1] = make_float2(o[i][2 * c + 1].x + a.z, o[i][2 * c + 1].y + a.w);
         }
@@ -818,7 +824,7 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
         for (int e = 0; e < 8; ++e) sq = fmaf(o[i][e].x, o[i][e].x, fmaf(o[i][e].y, o[i][e].y, sq));
         for (int w = 4; w; w >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, w);
         const float f = p.gain ? 1.0f / sqrtf(sq * (1.0f / VD) + p.eps) : 1.0f;
-        const int qi = q0 + 8 * ty + i;
+        const int qi = q0 + R * ty + i;
         if (qi < ce) {
             float *dst = static_cast<float *>(p.out) + qi * p.out_token + h * p.out_head;
 #pragma unroll
@@ -899,8 +905,9 @@ cudaError_t diff_attention_prepare(int device) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, DIFF_SMEM);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_diff_attention_f32, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_diff_attention_f32<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_diff_attention_f32<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
     if (e == cudaSuccess && device >= 0 && device < 64) done[device].store(true, std::memory_order_release);
     return e;
 }
@@ -908,8 +915,13 @@ cudaError_t diff_attention_prepare(int device) {
 cudaError_t launch_diff_attention(const DiffOp &op, const DiffMaps *maps, int num_sms, cudaStream_t st) {
     if (op.n_tokens <= 0 || op.n_rows <= 0) return cudaSuccess;
     if (op.qk_dtype == JD_F32) {
-        const dim3 grid(op.n_tokens / FQ + op.n_rows, op.heads);
-        k_diff_attention_f32<<<grid, F32_THREADS, F32_SMEM, st>>>(op);
+        // 64 queries a CTA unless two an SM would not be had: then 32, on twice the CTAs (8 rows of 200 to 300 with
+        // four heads, 157 CTAs: 73 against 118 us; 16 such rows, 314 CTAs: 132 against 127)
+        const int64_t ctas = ((int64_t)op.n_tokens / 64 + op.n_rows) * op.heads;
+        if (ctas > 2 * num_sms)
+            k_diff_attention_f32<8><<<dim3(op.n_tokens / 64 + op.n_rows, op.heads), F32_THREADS, F32_SMEM, st>>>(op);
+        else
+            k_diff_attention_f32<4><<<dim3(op.n_tokens / 32 + op.n_rows, op.heads), F32_THREADS, F32_SMEM, st>>>(op);
         return cudaGetLastError();
     }
     const int64_t items = ((int64_t)op.n_tokens / TQ + op.n_rows) * op.heads;
@@ -938,7 +950,7 @@ extern "C" jd_status jd_diff_attention(const jd_diff_attention_args *a, void *st
         return fail(JD_ERR_INVALID_ARG, "heads: out.n_heads 1..32767, a multiple of kv_heads");
     if (a->q.n_heads != 2 * heads || a->k.n_heads != 2 * kv || a->v.n_heads != kv)
         return fail(JD_ERR_INVALID_ARG, "heads: q has 2 heads, k 2 kv_heads, v kv_heads");
-    if (a->n_tokens > (1 << 30) || ((int64_t)a->n_tokens / 64 + a->n_rows) * heads > INT32_MAX - 65536)
+    if (a->n_tokens > (1 << 30) || ((int64_t)a->n_tokens / 32 + a->n_rows) * heads > INT32_MAX - 65536)
         return fail(JD_ERR_INVALID_ARG, "too many tokens, rows and heads");
     if (!std::isfinite(a->lambda_init) || !(a->norm_eps >= 0) || !std::isfinite(a->norm_eps) || !(a->scale >= 0) ||
         !std::isfinite(a->scale))

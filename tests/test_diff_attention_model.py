@@ -34,7 +34,7 @@ def find_row(starts, b):
     return lo
 
 
-@pytest.mark.parametrize("tile", [128, 64])
+@pytest.mark.parametrize("tile", [128, 64, 32])
 def test_every_query_tile_is_found_once(tile):
     rng = random.Random(1)
     for case in range(300):
