@@ -32,7 +32,7 @@
 // Rounding of P.  P enters the PV product in 16 bits.  With FP16 values and a BF16 result P in FP16
 // (2^-12) disappears behind the result's 2^-9.  Otherwise P's rounding would be as large as the
 // result's own and, since D is a difference, up to (1 + lambda) / (1 - lambda) times larger after
-// the norm: there P goes in as a pair hi + lo (lo in S's other 64 columns), twice the MMAs of PV.
+// the norm: there P goes in as a pair hi + lo (lo in the S tile's other 32 columns), twice the MMAs of PV.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (grows) m = mx;
                     __syncwarp();
                     const float mm = m == -INFINITY ? 0.f : m;  // nothing seen yet: every P is 0
-                    float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+                    float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
                     uint32_t pk[32], pl[SPLIT ? 32 : 1];
 #pragma unroll
                     for (int e = 0; e < TK; e += 2) {
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             fma_f32x2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
                                       make_float2(sl2, sl2), make_float2(-mm, -mm));
                         const float2 pv = make_float2(exp2_fast(xv.x), exp2_fast(xv.y));
-                        ls[(e >> 1) & 3] = add_f32x2(ls[(e >> 1) & 3], pv);
+                        ls[(e >> 1) & 1] = add_f32x2(ls[(e >> 1) & 1], pv);
                         pk[e >> 1] = pack_p<V16>(pv.x, pv.y);
                         if (SPLIT) {
                             const float2 h = unpack_p<V16>(pk[e >> 1]);
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     tmem_st32(ts, pk);
                     if constexpr (SPLIT) tmem_st32(ts + 32, pl);
-                    l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+                    l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                     tmem_st_wait();
                     tc_fence_before();
                 }
