@@ -950,7 +950,8 @@ extern "C" jd_status jd_diff_attention(const jd_diff_attention_args *a, void *st
         return fail(JD_ERR_INVALID_ARG, "heads: out.n_heads 1..32767, a multiple of kv_heads");
     if (a->q.n_heads != 2 * heads || a->k.n_heads != 2 * kv || a->v.n_heads != kv)
         return fail(JD_ERR_INVALID_ARG, "heads: q has 2 heads, k 2 kv_heads, v kv_heads");
-    if (a->n_tokens > (1 << 30) || ((int64_t)a->n_tokens / 32 + a->n_rows) * heads > INT32_MAX - 65536)
+    // (a query tile of a row of 2^24 takes a quarter of a second, which the kernel's bounded waits of two allow for)
+    if (a->n_tokens > (1 << 24) || ((int64_t)a->n_tokens / 32 + a->n_rows) * heads > INT32_MAX - 65536)
         return fail(JD_ERR_INVALID_ARG, "too many tokens, rows and heads");
     if (!std::isfinite(a->lambda_init) || !(a->norm_eps >= 0) || !std::isfinite(a->norm_eps) || !(a->scale >= 0) ||
         !std::isfinite(a->scale))

@@ -726,6 +726,7 @@ jd_status rotary_call(const jd_rotary_args *a, const jd_head_norm *norm, void *s
     if (a->head_dim < 2 || a->head_dim > 2 * ROTARY_MAX_PAIRS)
         return fail(JD_ERR_INVALID_ARG, "head_dim %d: 2..256 is required", a->head_dim);
     if (a->n_tokens < 0 || a->n_rows < 0) return fail(JD_ERR_INVALID_ARG, "negative n_tokens or n_rows");
+    if (a->n_tokens > (1 << 30)) return fail(JD_ERR_INVALID_ARG, "too many tokens: 2^30 at most");
     if (a->q.n_heads < 1 || a->k.n_heads < 0 || a->q.n_heads > 65536 || a->k.n_heads > 65536)
         return fail(JD_ERR_INVALID_ARG, "heads: q 1..65536, k 0..65536");
     if (a->q_out.n_heads != a->q.n_heads || a->k_out.n_heads != a->k.n_heads)

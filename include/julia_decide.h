@@ -504,7 +504,7 @@ typedef struct {
     jd_rotary_config rotary;
     int32_t dtype;            /* jd_dtype of q, k and their outputs */
     int32_t head_dim;         /* 2 .. 256 */
-    int32_t n_tokens, n_rows; /* >= 0; no tokens: nothing is done */
+    int32_t n_tokens, n_rows; /* >= 0, tokens at most 2^30; no tokens: nothing is done */
     const int32_t *positions, *cu_seqlens;
     jd_heads q, k, q_out, k_out;
 } jd_rotary_args;
@@ -536,7 +536,8 @@ jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm
  * pairs: head h has queries 2h and 2h + 1, and with kv head g = h / (heads /
  * kv_heads) keys 2g and 2g + 1 and the 128 wide values g.  Key j is seen by
  * query i of the same row if window < 0 or |i - j| <= window; a row sees no
- * other row, whatever the other holds.  Rows may be empty; nothing is written
+ * other row, whatever the other holds.  (Within a row a key that a window hides
+ * counts with weight 0, so its values must be finite.)  Rows may be empty; nothing is written
  * for tokens past cu_seqlens[n_rows].
  *   Types: q and k JD_BF16 or JD_F16 with v JD_BF16 or JD_F16, on the tensor
  *   cores with FP32 sums; or all JD_F32 (FP32 arithmetic).  out has q's type.
@@ -549,7 +550,7 @@ jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm
  * bounded wait that expired (1); the caller clears it. */
 typedef struct {
     int32_t qk_dtype, v_dtype;
-    int32_t n_tokens, n_rows;  /* >= 0; no tokens or rows: nothing is done */
+    int32_t n_tokens, n_rows;  /* >= 0, tokens at most 2^24; no tokens or rows: nothing is done */
     int32_t kv_heads;          /* out.n_heads (heads) is a multiple of it */
     int32_t window;
     const int32_t *cu_seqlens; /* device [n_rows + 1], ascending from 0 */

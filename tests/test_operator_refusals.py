@@ -37,6 +37,7 @@ def _rotary(**kw):
 @pytest.mark.parametrize("change,word", [
     (dict(dtype=3), "dtype"), (dict(head_dim=1), "head_dim"), (dict(head_dim=257), "head_dim"),
     (dict(n_tokens=-1), "negative"), (dict(n_rows=-1), "negative"), (dict(n_rows=0), "cu_seqlens"),
+    (dict(n_tokens=(1 << 30) + 1), "too many"),
     (dict(cu_seqlens=None), "cu_seqlens"), (dict(q__n_heads=0), "heads"), (dict(k__n_heads=-1), "heads"),
     (dict(q_out__n_heads=5), "n_heads"), (dict(k_out__n_heads=7), "n_heads"),
     (dict(q__data=None), "NULL"), (dict(k_out__data=None), "NULL"),
@@ -158,7 +159,7 @@ def _diff(**kw):
     (dict(qk_dtype=0), "v_dtype"), (dict(n_tokens=-1), "negative"), (dict(n_rows=-2), "negative"),
     (dict(kv_heads=0), "heads"), (dict(kv_heads=2), "heads"), (dict(out__n_heads=0), "heads"),
     (dict(q__n_heads=5), "heads"), (dict(k__n_heads=3), "heads"), (dict(v__n_heads=6), "heads"),
-    (dict(n_tokens=(1 << 30) + 1), "too many"), (dict(n_rows=1 << 30), "too many"),
+    (dict(n_tokens=(1 << 24) + 1), "too many"), (dict(n_rows=1 << 30), "too many"),
     (dict(lambda_init=float("nan")), "lambda_init"), (dict(norm_eps=-1.0), "norm_eps"),
     (dict(scale=float("inf")), "scale"), (dict(scale=-0.125), "scale"), (dict(q__token_stride=0), "strides"), (dict(k__head_stride=0), "strides"),
     (dict(v__token_stride=-8), "strides"), (dict(q__head_stride=1 << 39), "strides"),
