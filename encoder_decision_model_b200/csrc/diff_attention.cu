@@ -8,7 +8,7 @@
 //   warp 0          TMA producer: the item's Q_0, Q_1 (two buffers), K_0 and K_1 tiles of 64 keys (a ring
 //                   of 8 KB units, freed when their S product completes), V tiles (64 keys x 128, a
 //                   ring of 16 KB stages)
-//   warp 1, warp 3  lane 0 issues the tcgen05.mma of map 0 and of map 1 (warp 1 holds the TMEM):
+//   warp 1, warp 3  one lane issues the tcgen05.mma of map 0 and of map 1 (warp 1 holds the TMEM):
 //                     S_x = Q_x K_x^T  (M 128, N 64, K 64)
 //                     O_x += P_x V     (M 128, N 128, K 64; P from TMEM, V read MN-major)
 //   warp 2          zeroes the rows of an item's last V tile that lie past its keys: their
@@ -20,13 +20,19 @@
 // that its next scores are there while it works on these; P_x overwrites its S tile (the thread that
 // stores a row's P has read all of its S).
 //
-// What did not pay, on 16 rows of 8192 (2.8 to 3.0 ms, with the clock under the power cap): one S tile of 128
-// keys a map, whose next product waits for P V (3.1 ms); one thread issuing the MMAs of both maps, or not elected by
-// elect.sync, at a hundred clocks an MMA (5.7 ms); two threads a row (2.7 to 3.0 ms, but 10 % slower on rows of 550);
-// asking for the next S before P is handed over (3.0 ms); a quarter of the exponentials as polynomials on the FMA pipe
-// (3.1 ms: the softmax warps are bound by issued instructions and their latencies, not by the exponential unit).
+// Measured: 16 rows of 8192 with three heads and FP16 values 2.86 ms under the power cap (864 TFLOP/s,
+// 0.53 of the measured burst rate; single runs 2.6 to 2.8 ms), 256 rows of 64 to 1024 with BF16 values
+// 434 to 490 us, with a window of 64 and FP16 values 177 us.  On the long rows a step of 64 keys takes a
+// softmax warp 1,780 clocks: 915 of exponentials (two warps a scheduler share the unit), 310 waiting
+// for S, 330 for its read and the maximum, 230 for handing P over.  What did not pay, each against the
+// kernel as it was then: one thread issuing the MMAs of both maps (5.7 ms), or not elected by elect.sync
+// (603 against 511 us on the ragged rows); one S tile of 128 keys a map, whose next product waits for P V
+// (852 against 636 us there); two threads a row (long rows the same, ragged ones 10 % slower); asking
+// for the next S before P is handed over (3.1 against 3.0 ms); a quarter of the exponentials as
+// polynomials on the FMA pipe (2 to 8 % slower: the warps are bound by instructions and their
+// latencies, not by the exponential unit alone).
 //
-// Bound: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
+// Floor: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
 // exponentials a clock and SM, 0.094 and 0.125 clocks.
 //
 // Rounding of P.  P enters the PV product in 16 bits.  With FP16 values and a BF16 result P in FP16
@@ -651,8 +657,11 @@ static_assert(64 * 132 <= 2 * 64 * QP, "the second map's O lies over Q");
 // 8 R queries of one row and head against its keys, 64 at a time; two warps a map.  A thread holds R x 8
 // scores and R x 16 outputs of the same rows, so that a row's running maximum and sum stay with it and
 // its seven neighbours.  Shared memory hands a lane one float a clock against four FMAs: with R = 8 the
-// scores take 4 FMAs a float, the outputs 5.3; R = 4 is for calls too small to fill the SMs with that.  Q, K and P lie transposed (element-major), whole vectors a step; P
-// takes K's place.  Bound by FP32 arithmetic, 1536 operations a visible pair and head; two CTAs an SM.
+// scores take 4 FMAs a float, the outputs 5.3; R = 4 is for calls too small to fill the SMs with that.
+// Q, K and P lie transposed (element-major), whole vectors a step; P takes K's place.  Two CTAs an SM.
+// Bound by FP32 arithmetic, 768 operations a visible pair and head, the FMA pipe active 52 % of the cycles:
+// 24 rows of 64 to 512 with four heads 348 us, two rows of 8192 10.5 ms (39 TFLOP/s).  With 4 x 4 scores
+// and 4 x 8 outputs of both maps in every thread these took 415 us and 14.1 ms.
 template <int R>
 __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __grid_constant__ DiffOp p) {
     constexpr int FQ = 8 * R, SHIFT = R == 8 ? 6 : 5;
