@@ -214,11 +214,11 @@ __device__ __forceinline__ Item find_item(const DiffOp &p, int w, int lane, int 
     for (;;) {
         const int at = lo + lane, v = p.cu[min(at, p.n_rows)];
         const unsigned below = __ballot_sync(0xffffffffu, at < p.n_rows && (v >> 7) + at <= b);
-        if (below == 0xffffffffu && lo + 32 < p.n_rows) {
+        if (below == 0xffffffffu) {  // lane 31 then lies before n_rows: after the step lane 0 does
             lo += 31;
             continue;
         }
-        const int k = min(31 - __clz(below | 1u), 30);
+        const int k = 31 - __clz(below | 1u);  // at most 30: lane k + 1 holds the row's end
         t.cs = max(__shfl_sync(0xffffffffu, v, k), 0);
         t.ce = min(__shfl_sync(0xffffffffu, v, k + 1), p.n_tokens);
         lo += k;
