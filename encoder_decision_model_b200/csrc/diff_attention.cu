@@ -35,10 +35,12 @@
 // Floor: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
 // exponentials a clock and SM, 0.094 and 0.125 clocks.
 //
-// Rounding of P.  P enters the PV product in 16 bits.  With FP16 values and a BF16 result P in FP16
-// (2^-12) disappears behind the result's 2^-9.  Otherwise P's rounding would be as large as the
-// result's own and, since D is a difference, up to (1 + lambda) / (1 - lambda) times larger after
-// the norm: there P goes in as a pair hi + lo (lo in the S tile's other 32 columns), twice the MMAs of PV.
+// Rounding of P.  P enters the PV product as a pair of 16-bit numbers hi + lo (lo in the S tile's other 32
+// columns), twice the MMAs of PV: 2^-22 of it is lost in FP16, 2^-16 in BF16.  One number alone would lose 2^-11 or
+// 2^-8, and D is a difference: where the two maps are alike the norm makes that up to (1 + lambda) / (1 - lambda)
+// times larger, 9 times at the lambda of 0.8 of deep layers and without bound towards 1, however long the row.
+// Emulated in 64 bits with P as one FP16 number, nearly equal maps and FP16 values, elements of a BF16 result were off by up
+// to 47 half steps at lambda 0.8 and 160 at 0.95 (rows of 2 to 512 keys); with the pair the sums' own error is what is left.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -256,8 +258,8 @@ __device__ __forceinline__ float2 unpack_p(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// V16: FP16 values; SPLIT: P as hi + lo
-template <bool V16, bool SPLIT>
+// V16: FP16 values, else BF16
+template <bool V16>
 __global__ void __launch_bounds__(THREADS, 1)
     k_diff_attention(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DiffOp p, int n_items) {
@@ -409,11 +411,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const int steps = last ? (now.in_last() + 15) >> 4 : TK / 16;
                         if (steps == TK / 16) {
                             mma_pv(o, pt, v, idesc_pv, j);
-                            if (SPLIT) mma_pv(o, pt + 32, v, idesc_pv, 1);
+                            mma_pv(o, pt + 32, v, idesc_pv, 1);
                         } else {
                             for (int ks = 0; ks < steps; ++ks) {
                                 mma_ts(o, pt + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, j | ks);
-                                if (SPLIT) mma_ts(o, pt + 32 + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, 1);
+                                mma_ts(o, pt + 32 + 8 * ks, v + ks * (16 * 128 >> 4), idesc_pv, 1);
                             }
                         }
                         commit(b_pvdone + 8 * b);
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     uint32_t zero[32] = {};
                     tmem_st32(ts, zero);
-                    if constexpr (SPLIT) tmem_st32(ts + 32, zero);
+                    tmem_st32(ts + 32, zero);
                     tmem_st_wait();
                     tc_fence_before();
                 } else if (!dead) {
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     const float mm = m == -INFINITY ? 0.f : m;  // nothing seen yet: every P is 0
                     float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    uint32_t pk[32], pl[SPLIT ? 32 : 1];
+                    uint32_t pk[32], pl[32];  // hi, lo
 #pragma unroll
                     for (int e = 0; e < TK; e += 2) {
                         const float2 xv =
@@ -520,13 +522,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const float2 pv = make_float2(exp2_fast(xv.x), exp2_fast(xv.y));
                         ls[(e >> 1) & 1] = add_f32x2(ls[(e >> 1) & 1], pv);
                         pk[e >> 1] = pack_p<V16>(pv.x, pv.y);
-                        if (SPLIT) {
-                            const float2 h = unpack_p<V16>(pk[e >> 1]);
-                            pl[e >> 1] = pack_p<V16>(pv.x - h.x, pv.y - h.y);
-                        }
+                        const float2 h = unpack_p<V16>(pk[e >> 1]);
+                        pl[e >> 1] = pack_p<V16>(pv.x - h.x, pv.y - h.y);
                     }
                     tmem_st32(ts, pk);
-                    if constexpr (SPLIT) tmem_st32(ts + 32, pl);
+                    tmem_st32(ts + 32, pl);
                     l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                     tmem_st_wait();
                     tc_fence_before();
@@ -848,10 +848,8 @@ __global__ void __launch_bounds__(F32_THREADS, 2) k_diff_attention_f32(const __g
 }
 
 const void *tensor_kernel(const DiffOp &op) {
-    const bool v16 = op.v_dtype == JD_F16, split = !(v16 && op.qk_dtype == JD_BF16);
-    if (!v16) return reinterpret_cast<const void *>(&k_diff_attention<false, true>);
-    return split ? reinterpret_cast<const void *>(&k_diff_attention<true, true>)
-                 : reinterpret_cast<const void *>(&k_diff_attention<true, false>);
+    return op.v_dtype == JD_F16 ? reinterpret_cast<const void *>(&k_diff_attention<true>)
+                                : reinterpret_cast<const void *>(&k_diff_attention<false>);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -902,9 +900,8 @@ jd_status make_diff_maps(const DiffOp &op, DiffMaps *maps) {
 cudaError_t diff_attention_prepare(int device) {
     static std::atomic<bool> done[64];
     if (device >= 0 && device < 64 && done[device].load(std::memory_order_acquire)) return cudaSuccess;
-    const void *kernels[3] = {reinterpret_cast<const void *>(&k_diff_attention<false, true>),
-                              reinterpret_cast<const void *>(&k_diff_attention<true, true>),
-                              reinterpret_cast<const void *>(&k_diff_attention<true, false>)};
+    const void *kernels[2] = {reinterpret_cast<const void *>(&k_diff_attention<false>),
+                              reinterpret_cast<const void *>(&k_diff_attention<true>)};
     for (const void *k : kernels) {
         // a group asking for more registers than the launch holds would wait for ever
         cudaFuncAttributes fa;

@@ -541,9 +541,9 @@ jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm
  * for tokens past cu_seqlens[n_rows].
  *   Types: q and k JD_BF16 or JD_F16 with v JD_BF16 or JD_F16, on the tensor
  *   cores with FP32 sums; or all JD_F32 (FP32 arithmetic).  out has q's type.
- *   The probabilities enter the second product as FP16 or BF16, as v is; as a
- *   pair of those (16 bits of mantissa or more) where one alone would show
- *   beside the rounding of out.
+ *   There the probabilities enter the second product as a pair of FP16 or BF16
+ *   numbers, as v is: 16 bits of mantissa or more (FP16: down to 2^-25 of a
+ *   row's largest).
  *   Pointers and strides lie on 16-byte multiples; input strides are positive.
  *   out must not overlap an input.
  * `status` (device, may be NULL) collects the bits of jd_check_status: a
