@@ -520,7 +520,7 @@ def jd_diff_attention(q, k, v, out, cu_seqlens, lambda_q1, lambda_k1, lambda_q2,
                       norm_eps=1e-5, window=-1, scale=0.0, status=None, stream=None):
     """Differential attention inside each packed row.  q [tokens, 2 heads, 64], k [tokens, 2 kv_heads, 64], v [tokens,
     kv_heads, 128], out [tokens, heads, 128]; the lambda vectors (64) and norm_gain (128) are float32; window < 0 for
-    the whole row; status: an int32 device tensor that collects failed checks, or None."""
+    the whole row; status: an int32 device tensor that collects failed checks, or None (they are not reported then)."""
     hq, hk, hv, ho = _heads(q), _heads(k), _heads(v), _heads(out)
     T, dtype, kv = q.shape[0], q.dtype, hv[3]
     if k.dtype != dtype or out.dtype != dtype:

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
              *odone = pvdone + 4, *summed = odone + 2, *ofree = summed + 2;  // sfull, pready, pvdone: 2 map + tile % 2; odone: map
     float *gain = reinterpret_cast<float *>(smem + OFF_F), *sums = gain + 128;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sums + 512);
-    unsigned *own_status = tmem_slot + 1;
+    unsigned *status = tmem_slot + 1;  // expired waits of this CTA: the caller's word may hold another call's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&pvdone[i], 1);
         }
         mbar_init(ofree, 4);
-        *own_status = 0;
+        *status = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
         prefetch_tmap(&tm_q);
@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    unsigned *status = p.status ? p.status : own_status;
     int row = 0;  // where this warp's search for items has got to
     if (warp < 4) {  // warp group 0: producers, MMA issue, the tail of V
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_ROLES));
@@ -639,6 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     __syncthreads();
+    if (threadIdx.x == 0 && p.status && *status) atomicOr(p.status, *status);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

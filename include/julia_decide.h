@@ -547,7 +547,9 @@ jd_status jd_qk_norm_rotary(const jd_rotary_args *args, const jd_head_norm *norm
  *   Pointers and strides lie on 16-byte multiples; input strides are positive.
  *   out must not overlap an input.
  * `status` (device, may be NULL) collects the bits of jd_check_status: a
- * bounded wait that expired (1); the caller clears it. */
+ * bounded wait that expired (1), which leaves the output unfinished; the caller
+ * clears it.  Bits that it holds before do not change a call.  With NULL an
+ * expired wait is not reported. */
 typedef struct {
     int32_t qk_dtype, v_dtype;
     int32_t n_tokens, n_rows;  /* >= 0, tokens at most 2^24; no tokens or rows: nothing is done */
