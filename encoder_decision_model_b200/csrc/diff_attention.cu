@@ -79,6 +79,9 @@ constexpr int THREADS = 16 * 32;
 // launch: a warp group asking for more than the launch holds would wait for ever); the warp groups of the
 // roles and of the read-out give up some, which the softmax groups take.
 constexpr int REGS = 128, REGS_ROLES = 72, REGS_READOUT = 104, REGS_SOFTMAX = 160;
+// After an expired wait: how long a block stays, for its copies and products in flight (microseconds, if they come at all).
+constexpr int LINGER_STEPS = 100'000;
+constexpr uint64_t LINGER_NS = 20'000'000;
 constexpr int BAR_GAIN = 1;  // named barrier of the read-out warps
 static_assert(128 * (REGS_ROLES + REGS_READOUT) + 256 * REGS_SOFTMAX <= THREADS * REGS, "register split");
 
@@ -639,6 +642,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncthreads();
     if (threadIdx.x == 0 && p.status && *status) atomicOr(p.status, *status);
+    if (*status) {
+        const uint64_t from = globaltimer_ns();
+        for (int i = 0; i < LINGER_STEPS && globaltimer_ns() - from < LINGER_NS; ++i) __nanosleep(1000);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
