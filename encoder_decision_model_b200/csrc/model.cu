@@ -673,7 +673,8 @@ jd_status alloc_workspace(jd_model *m) {
         TRY(make_map(&m->to_ym, m->ym, HFF, M, HFF, 64, 32));
         TRY(make_diff_maps(diff_op(m->qkv, m->o, (int)T, false), &m->tm_diff));
     }
-    CK(diff_attention_prepare(m->device));
+    const bool diff = std::any_of(std::begin(m->lam), std::end(m->lam), [](const float *p) { return p != nullptr; });
+    if (diff) CK(diff_attention_prepare(m->device));
     return JD_OK;
 }
 
