@@ -464,6 +464,9 @@ def _vector(t, kind, n, name):
 def rotary_config(dims, theta, layout="half", scaling="none", factor=1.0, original_length=8192, beta_fast=32.0,
                   beta_slow=1.0):
     """jd_rotary_config; layout and scaling by name ("half" / "interleaved", "none" / "linear" / "ntk" / "yarn")."""
+    for name, n in (("dims", dims), ("original_length", original_length)):
+        if not -(1 << 31) <= n < 1 << 31:  # ctypes would wrap it around
+            raise _bad(f"rotary {name} {n} is out of range")
     try:
         return jd_rotary_config(_LAYOUTS[layout], dims, theta, _SCALINGS[scaling], original_length, factor, beta_fast,
                                 beta_slow)
@@ -476,6 +479,13 @@ _HEADS = "Pqqi4x"
 _ROTARY_ARGS = struct.Struct("@iidiiddd" + "iiii" + "PP" + 4 * _HEADS)
 _HEAD_NORM = struct.Struct("@ifPP")
 _DIFF_ARGS = struct.Struct("@iiiiiiP" + 4 * _HEADS + "PPPPPfff4xP")
+
+
+def _pack(record, *values):
+    try:
+        return record.pack(*values)
+    except struct.error as e:
+        raise _bad(f"an argument does not fit: {e}") from None
 
 
 def _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions):
@@ -493,10 +503,10 @@ def _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions):
         hko = _heads(k_out, (ks, dtype))
     n_rows = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     r = rotary
-    return _ROTARY_ARGS.pack(r.layout, r.dims, r.theta, r.scaling, r.original_length, r.factor, r.beta_fast,
-                             r.beta_slow, _dtype(q), d, T, n_rows, _vector(positions, "int32", T, "positions"),
-                             _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"), *hq, *hk,
-                             *_heads(q_out, (shape, dtype)), *hko), d
+    return _pack(_ROTARY_ARGS, r.layout, r.dims, r.theta, r.scaling, r.original_length, r.factor, r.beta_fast,
+                 r.beta_slow, _dtype(q), d, T, n_rows, _vector(positions, "int32", T, "positions"),
+                 _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"), *hq, *hk,
+                 *_heads(q_out, (shape, dtype)), *hko), d
 
 
 def jd_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=None, positions=None, stream=None):
@@ -512,7 +522,7 @@ def jd_qk_norm_rotary(q, k, q_out, k_out, rotary: jd_rotary_config, cu_seqlens=N
     a, d = _rotary_args(q, k, q_out, k_out, rotary, cu_seqlens, positions)
     if norm not in _NORMS:
         raise _bad(f"unknown norm {norm!r}")
-    n = _HEAD_NORM.pack(_NORMS[norm], eps, _vector(q_gain, JD_F32, d, "q_gain"), _vector(k_gain, JD_F32, d, "k_gain"))
+    n = _pack(_HEAD_NORM, _NORMS[norm], eps, _vector(q_gain, JD_F32, d, "q_gain"), _vector(k_gain, JD_F32, d, "k_gain"))
     _check(lib().jd_qk_norm_rotary(a, n, _stream(stream)))
 
 
@@ -530,11 +540,12 @@ def jd_diff_attention(q, k, v, out, cu_seqlens, lambda_q1, lambda_k1, lambda_q2,
     if q.shape[2] != 64 or k.shape[2] != 64 or v.shape[2] != 128 or out.shape[2] != 128:
         raise _bad("query and key heads are 64 wide, values and outputs 128")
     n_rows = cu_seqlens.numel() - 1
-    a = _DIFF_ARGS.pack(_dtype(q), _dtype(v), T, n_rows, kv, window, _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"),
-                        *hq, *hk, *hv, *ho, _vector(lambda_q1, JD_F32, 64, "lambda_q1"),
-                        _vector(lambda_k1, JD_F32, 64, "lambda_k1"), _vector(lambda_q2, JD_F32, 64, "lambda_q2"),
-                        _vector(lambda_k2, JD_F32, 64, "lambda_k2"), _vector(norm_gain, JD_F32, 128, "norm_gain"),
-                        lambda_init, norm_eps, scale, _vector(status, "int32", 1, "status"))
+    a = _pack(_DIFF_ARGS, _dtype(q), _dtype(v), T, n_rows, kv, window,
+              _vector(cu_seqlens, "int32", n_rows + 1, "cu_seqlens"), *hq, *hk, *hv, *ho,
+              _vector(lambda_q1, JD_F32, 64, "lambda_q1"), _vector(lambda_k1, JD_F32, 64, "lambda_k1"),
+              _vector(lambda_q2, JD_F32, 64, "lambda_q2"), _vector(lambda_k2, JD_F32, 64, "lambda_k2"),
+              _vector(norm_gain, JD_F32, 128, "norm_gain"), lambda_init, norm_eps, scale,
+              _vector(status, "int32", 1, "status"))
     _check(lib().jd_diff_attention(a, _stream(stream)))
 
 
