@@ -20,11 +20,12 @@
 // that its next scores are there while it works on these; P_x overwrites its S tile (the thread that
 // stores a row's P has read all of its S).
 //
-// Measured: 16 rows of 8192 with three heads and FP16 values 2.86 ms under the power cap (864 TFLOP/s,
-// 0.53 of the measured burst rate; single runs 2.6 to 2.8 ms), 256 rows of 64 to 1024 with BF16 values
-// 434 to 490 us, with a window of 64 and FP16 values 177 us.  On the long rows a step of 64 keys takes a
-// softmax warp 1,780 clocks: 915 of exponentials (two warps a scheduler share the unit), 310 waiting
-// for S, 330 for its read and the maximum, 230 for handing P over.  What did not pay, each against the
+// Measured: 16 rows of 8192 with three heads and FP16 values 3.74 to 3.79 ms one after another (660
+// TFLOP/s, 0.40 of the measured burst rate), single runs 3.3 to 3.6 ms; 256 rows of 64 to 1024 with BF16
+// values 433 us in a few calls, 468 to 483 after hundreds in a row, with FP16 values 483 to 503; with a
+// window of 64 and FP16 values 218 to 231 us.  On the long rows a step of 64 keys takes a softmax warp 2,080 clocks:
+// 1,130 to 1,180 of exponentials, their rounding and packing (two warps a scheduler share the units), 290 to 320 waiting
+// for S, 350 for its read and the maximum, 260 for handing P over.  What did not pay, each against the
 // kernel as it was then: one thread issuing the MMAs of both maps (5.7 ms), or not elected by elect.sync
 // (603 against 511 us on the ragged rows); one S tile of 128 keys a map, whose next product waits for P V
 // (852 against 636 us there); two threads a row (long rows the same, ragged ones 10 % slower); asking
@@ -33,7 +34,7 @@
 // latencies, not by the exponential unit alone).
 //
 // Floor: 768 FLOP and two exponentials a visible (query, key) pair and head; at 8192 FLOP and 16
-// exponentials a clock and SM, 0.094 and 0.125 clocks.
+// exponentials a clock and SM, 0.094 and 0.125 clocks (0.156 for the 1,280 FLOP that a pair P costs).
 //
 // Rounding of P.  P enters the PV product as a pair of 16-bit numbers hi + lo (lo in the S tile's other 32
 // columns), twice the MMAs of PV: 2^-22 of it is lost in FP16, 2^-16 in BF16.  One number alone would lose 2^-11 or

@@ -11,9 +11,9 @@
 // Angles are formed, not read from a table: p * w_j is reduced to a fraction of a turn in 64 bits, exact
 // for any position (in 32 bits the angle at position 10^5 is off by 4e-3); sine and cosine of the
 // fraction are FP32.  The pass reads and writes each element once and is bound by HBM: 131,072 tokens
-// of 12 heads of 64 in BF16 take 68 us (5.9 TB/s, 0.90 of the measured copy), 139,809 in FP16 with half
-// of each head interleaved 72 us (0.91); 556,823 with RMS norms 296 to 334 us (0.78 to 0.88), where the
-// issue slots are two thirds full.
+// of 12 heads of 64 in BF16 take 68 to 70 us (0.88 to 0.91 of the measured copy), 139,809 in FP16 with half
+// of each head interleaved 72 to 78 us (0.84 to 0.91); 556,823 with RMS norms 296 us in a few calls and 320 to 343
+// in a row (0.76 to 0.88), where the issue slots are two thirds full.
 //
 // Two kernels: k_rotary as above, where head_dim and the two runs fall on 16-byte vectors, and
 // k_rotary_any for every other width, offset and stride (a thread holds eight elements and finds
